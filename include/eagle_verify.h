@@ -345,12 +345,137 @@ eagle_status_t eagle_draft_child_rows(int32_t batch, int32_t rows_per_seq, int32
                                       float *child_probs, void *stream);
 
 /*
+ * ---------------------------------------------------------------- paged K/V cache
+ * The same verification step over a cache held in pages, as a server keeps it: a sequence's
+ * prefix lives on pages of a common pool, sequences may share pages, and new tokens need no
+ * contiguous room.  The pages have no counterpart of these entry points.
+ *
+ *   k_pages, v_pages  [num_pages, Hkv, page_size, D] dtype
+ *   page_table        [B, max_pages] int32 device: position p of sequence b is row
+ *                     p % page_size of page page_table[b][p / page_size]
+ * Entries of page_table past a sequence's length are never used.  A page index outside
+ * [0, num_pages) that is needed records device error 0x206.
+ */
+typedef struct {
+    int32_t num_pages;  /* pages in the pool, >= 1                                   */
+    int32_t page_size;  /* positions per page: 16, 32, 64, 128 or 256                */
+    int32_t max_pages;  /* page_table row stride, >= 1; max_pages * page_size < 2^31 */
+} eagle_pages_t;
+
+typedef struct {
+    int32_t table_len;    /* rows of cos_sin                                         */
+    int32_t rotary_dim;   /* rotated columns of a head: a multiple of 16, 0..D       */
+    int32_t interleaved;  /* 0: pairs (i, i + rotary_dim/2); 1: pairs (2i, 2i + 1)   */
+} eagle_rope_t;
+
+/*
+ * Rotary position embedding of a packed batch of token rows, and their append to the cache.
+ * For row r at position p = positions[r], every pair (a, b) of a query or key head turns into
+ *     (a cos(p, i) - b sin(p, i),  b cos(p, i) + a sin(p, i))     i < rotary_dim / 2
+ * (fp32 arithmetic, rounded once to dtype; columns past rotary_dim are copied), and with
+ * s = seq_ids[r] >= 0 the rotated key and the value are written to position p of sequence s.
+ *   q [R, Hq, D], k [R, Hkv, D], v [R, Hkv, D] dtype; *_stride = elements between rows (at
+ *     least the row's width, a multiple of 16 bytes), so they may be parts of one packed
+ *     projection.  q may be NULL (with q_out).
+ *   positions [R] int32; a negative one marks a padding row: nothing of it is read or written.
+ *     The rows of a call name different (sequence, position) slots; a slot named twice holds
+ *     a mixture of the two rows.
+ *   seq_ids   [R] int32, or NULL: nothing is appended (`pages`, v, k_pages, v_pages and
+ *     page_table are then not used).  -1 for a row that is only rotated.
+ *   cos_sin   [table_len, rotary_dim] fp32: the cosines of a position's rotary_dim/2 angles,
+ *     then their sines (unused with rotary_dim = 0).
+ *   q_out [R, Hq, D] dtype; k_out [R, Hkv, D] dtype or NULL: the rotated keys as a dense array
+ *     (the k_tree of a draft tree).  Either may be its own input if that is dense; otherwise
+ *     an output overlaps no input and not the other output.
+ * A row whose position lies outside the table or the cache, or whose sequence is outside
+ * [-1, B), is skipped whole and records device error 0x401 (0x206 for its page index).
+ * R = num_rows >= 0.  Uses shape's batch, heads, head_dim and dtype.  No workspace.
+ */
+eagle_status_t eagle_rope_append(const eagle_shape_t *shape, const eagle_pages_t *pages,
+                                 const eagle_rope_t *rope, int32_t num_rows, const void *q,
+                                 int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                 int64_t v_stride, const int32_t *positions,
+                                 const int32_t *seq_ids, const float *cos_sin, void *k_pages,
+                                 void *v_pages, const int32_t *page_table, void *q_out,
+                                 void *k_out, void *stream);
+
+/*
+ * eagle_tree_attention over the paged cache, for a batch whose sequences share their first
+ * `shared_len` positions (a system prompt): the shared part is read and computed once for
+ * the whole batch, every sequence's own part after it, and the parts are merged by their
+ * softmax statistics.  shared_len = 0 is plain paged tree attention; num_nodes = 1 with
+ * parents = -1 is the decoding of single tokens.
+ *   q, k_tree, v_tree, parents, out as for eagle_tree_attention
+ *   prefix_lens  [B] int32, whole lengths (the shared part included), each in
+ *                0..max_prefix_len (outside: clamped, device error 0x205)
+ *   shared_len   host value, 0..max_prefix_len.  The cache holds the same values at positions
+ *                [0, shared_len) of every sequence with prefix_lens[b] >= shared_len, by the
+ *                same pages or by copies; they are read through the table rows of some of
+ *                those sequences.  A sequence shorter than shared_len (a padding entry of
+ *                length 0, say) reads all its positions through its own table row.
+ *   workspace    >= eagle_paged_workspace_bytes(shape, pages, shared_len), 256-byte aligned
+ * Positions past a sequence's length are never used, whatever they hold.  A needed position
+ * on a page outside [0, num_pages) counts as a zero key and value.
+ * max_prefix_len <= max_pages * page_size.  Calls that may overlap need workspaces of their
+ * own, graphs that may run at the same time too.
+ */
+size_t eagle_paged_workspace_bytes(const eagle_shape_t *shape, const eagle_pages_t *pages,
+                                   int32_t shared_len);
+eagle_status_t eagle_tree_attention_paged(const eagle_shape_t *shape, const eagle_pages_t *pages,
+                                          const void *q, const void *k_pages, const void *v_pages,
+                                          const int32_t *page_table, const int32_t *prefix_lens,
+                                          int32_t shared_len, const void *k_tree,
+                                          const void *v_tree, const int32_t *parents, void *out,
+                                          void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * eagle_commit_accepted into pages: position L_b + t of sequence b receives the K/V of row t
+ * of the accepted path.  Arguments and outputs as there; the cache's capacity is
+ * max_pages * page_size, and new_prefix_lens[b] is -1 too (nothing written, device error
+ * 0x206) when one of the n positions has no page in the pool.  Sequences must not share the
+ * pages that receive new rows.
+ */
+eagle_status_t eagle_commit_accepted_paged(const eagle_shape_t *shape, const eagle_pages_t *pages,
+                                           void *k_pages, void *v_pages,
+                                           const int32_t *page_table, const int32_t *prefix_lens,
+                                           const void *k_tree, const void *v_tree,
+                                           const void *hidden, const int32_t *parents,
+                                           const int32_t *accepted_nodes,
+                                           const int32_t *accept_len, int32_t *new_prefix_lens,
+                                           void *feat, void *stream);
+
+/*
+ * ---------------------------------------------------------------- e4m3 LM head
+ * LM-head logits from 8-bit floating-point (e4m3) operands with one fp32 scale for each block
+ * of 128, half the weight bytes of the bf16 head:
+ *     logits[r, v] = sum_t x_scales[t, r] * w_scales[v / 128, t] * sum_{k in block t} x[r, k] * w[v, k]
+ * over the KB = ceil(H / 128) blocks of 128 columns (fp32 accumulation).
+ *   x         [R, H] e4m3, w [V, H] e4m3 (H a multiple of 16)
+ *   x_scales  [KB, ldm] fp32 with ldm = R rounded up to a multiple of 4 (entries past R unused)
+ *   w_scales  [ceil(V / 128), KB] fp32
+ *   logits    [R, V] fp32
+ * Any fp32 scales are taken; eagle_quantize_rows / eagle_quantize_blocks make them from dtype
+ * (eagle_dtype_t) values: per block the power of two 2^e with the smallest e >= -126 for which
+ * the block's largest magnitude is <= 448 * 2^e, elements rounded to nearest even after an
+ * exact division by it.  A block that holds an infinity or a NaN gets a NaN scale.  R = 0 is
+ * allowed and does nothing.  No workspace.
+ */
+eagle_status_t eagle_quantize_rows(int32_t rows, int32_t cols, int32_t dtype, const void *x,
+                                   void *x_out, float *x_scales, void *stream);
+eagle_status_t eagle_quantize_blocks(int32_t rows, int32_t cols, int32_t dtype, const void *w,
+                                     void *w_out, float *w_scales, void *stream);
+eagle_status_t eagle_lm_head_logits_scaled(int32_t rows, int32_t hidden, int32_t vocab,
+                                           const void *x, const float *x_scales, const void *w,
+                                           const float *w_scales, float *logits, void *stream);
+
+/*
  * Reads (and, if `reset` != 0, clears) the device error word that bounded waits set
  * when they give up.  Synchronises the current device.  *code = 0 means no error.
  * Codes: 0x101-0x103 an LM-head wait gave up; 0x201-0x203 a tree-attention wait gave up;
  * 0x204 a launch plan gave a compact attention CTA two tiles; 0x205 a prefix length
  * outside [0, Lmax] (clamped); 0x301 / 0x302 an accept-walk copy / cluster wait gave up;
- * 0x303 the CTAs of an accept-walk cluster disagreed and stopped.
+ * 0x303 the CTAs of an accept-walk cluster disagreed and stopped; 0x206 a page index outside
+ * the pool; 0x401 an append row outside the cache or the angle table (skipped).
  */
 eagle_status_t eagle_device_error(int32_t *code, int32_t reset);
 

@@ -25,7 +25,9 @@ EXPORTED = ("eagle_status_string", "eagle_workspace_bytes", "eagle_tree_attentio
             "eagle_lm_head_logits", "eagle_tree_accept", "eagle_verify_step",
             "eagle_commit_accepted", "eagle_tree_rerank", "eagle_draft_select",
             "eagle_draft_select_distinct", "eagle_draft_child_rows",
-            "eagle_device_error")
+            "eagle_rope_append", "eagle_paged_workspace_bytes", "eagle_tree_attention_paged",
+            "eagle_commit_accepted_paged", "eagle_quantize_rows", "eagle_quantize_blocks",
+            "eagle_lm_head_logits_scaled", "eagle_device_error")
 
 
 class Shape(ctypes.Structure):
@@ -42,6 +44,20 @@ def make_shape(batch, num_nodes, num_q_heads, num_kv_heads, head_dim, max_prefix
         dtype = {"f32": DTYPE_F32, "bf16": DTYPE_BF16}[dtype]
     return Shape(batch, num_nodes, num_q_heads, num_kv_heads, head_dim, max_prefix_len, hidden,
                  vocab, dtype, softmax_scale)
+
+
+class Pages(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("table_len", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+def make_pages(num_pages, page_size, max_pages) -> Pages:
+    return Pages(num_pages, page_size, max_pages)
 
 
 class EagleError(RuntimeError):
@@ -87,6 +103,21 @@ def load() -> ctypes.CDLL:
     L.eagle_draft_select_distinct.argtypes = [i32, i32, i32, i32, vp, f32, u64, u64, vp, vp, vp, vp]
     L.eagle_draft_child_rows.restype = ctypes.c_int
     L.eagle_draft_child_rows.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp]
+    pp, i64 = ctypes.POINTER(Pages), ctypes.c_int64
+    L.eagle_rope_append.restype = ctypes.c_int
+    L.eagle_rope_append.argtypes = [sp, pp, ctypes.POINTER(Rope), i32, vp, i64, vp, i64, vp, i64] + [vp] * 9
+    L.eagle_paged_workspace_bytes.restype = sz
+    L.eagle_paged_workspace_bytes.argtypes = [sp, pp, i32]
+    L.eagle_tree_attention_paged.restype = ctypes.c_int
+    L.eagle_tree_attention_paged.argtypes = [sp, pp] + [vp] * 5 + [i32] + [vp] * 5 + [sz, vp]
+    L.eagle_commit_accepted_paged.restype = ctypes.c_int
+    L.eagle_commit_accepted_paged.argtypes = [sp, pp] + [vp] * 13
+    L.eagle_quantize_rows.restype = ctypes.c_int
+    L.eagle_quantize_rows.argtypes = [i32, i32, i32, vp, vp, vp, vp]
+    L.eagle_quantize_blocks.restype = ctypes.c_int
+    L.eagle_quantize_blocks.argtypes = [i32, i32, i32, vp, vp, vp, vp]
+    L.eagle_lm_head_logits_scaled.restype = ctypes.c_int
+    L.eagle_lm_head_logits_scaled.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, vp]
     L.eagle_device_error.restype = ctypes.c_int
     L.eagle_device_error.argtypes = [ctypes.POINTER(i32), i32]
     _lib = L
@@ -204,6 +235,93 @@ def draft_child_rows(probs, tokens, child_probs, stream=None) -> None:
     k = tokens.shape[-1]
     _check("eagle_draft_child_rows", load().eagle_draft_child_rows(
         int(B), int(F), int(V), int(k), _ptr(probs), _ptr(tokens), _ptr(child_probs), _stream(stream)))
+
+
+# ---------------------------------------------------------------- paged cache
+
+def _rows(t):
+    """(pointer, row stride in elements) of a [R, heads, D] tensor whose rows may be strided
+    parts of a wider array."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        raise ValueError("library arguments are device tensors")
+    if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+        raise ValueError("token rows are [R, heads, D] with dense heads")
+    R, heads, d = t.shape
+    return t.data_ptr(), (t.stride(0) if R > 1 else heads * d)
+
+
+def rope_append(shape: Shape, pages: Optional[Pages], q, k, v, positions, seq_ids, cos_sin, k_pages,
+                v_pages, page_table, q_out, k_out=None, interleaved: bool = False, stream=None) -> None:
+    """cos_sin [table_len, rotary_dim], or None for rotary_dim 0; seq_ids None: rotation only."""
+    rope = Rope(0, 0, 0) if cos_sin is None else Rope(cos_sin.shape[0], cos_sin.shape[1], int(interleaved))
+    qp, qs = _rows(q)
+    kp, ks = _rows(k)
+    vp, vs = _rows(v)
+    _check("eagle_rope_append", load().eagle_rope_append(
+        ctypes.byref(shape), None if pages is None else ctypes.byref(pages), ctypes.byref(rope),
+        positions.shape[0], qp, qs, kp, ks, vp, vs, _ptr(positions), _ptr(seq_ids), _ptr(cos_sin),
+        _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(q_out), _ptr(k_out), _stream(stream)))
+
+
+def paged_workspace_bytes(shape: Shape, pages: Pages, shared_len: int) -> int:
+    return int(load().eagle_paged_workspace_bytes(ctypes.byref(shape), ctypes.byref(pages), int(shared_len)))
+
+
+def tree_attention_paged(shape: Shape, pages: Pages, q, k_pages, v_pages, page_table, prefix_lens,
+                         shared_len: int, k_tree, v_tree, parents, out, workspace=None,
+                         stream=None) -> None:
+    _check("eagle_tree_attention_paged", load().eagle_tree_attention_paged(
+        ctypes.byref(shape), ctypes.byref(pages), _ptr(q), _ptr(k_pages), _ptr(v_pages),
+        _ptr(page_table), _ptr(prefix_lens), int(shared_len), _ptr(k_tree), _ptr(v_tree),
+        _ptr(parents), _ptr(out), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def commit_accepted_paged(shape: Shape, pages: Pages, k_pages, v_pages, page_table, prefix_lens,
+                          k_tree, v_tree, hidden, parents, accepted_nodes, accept_len,
+                          new_prefix_lens, feat, stream=None) -> None:
+    _check("eagle_commit_accepted_paged", load().eagle_commit_accepted_paged(
+        ctypes.byref(shape), ctypes.byref(pages), _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
+        _ptr(prefix_lens), _ptr(k_tree), _ptr(v_tree), _ptr(hidden), _ptr(parents),
+        _ptr(accepted_nodes), _ptr(accept_len), _ptr(new_prefix_lens), _ptr(feat), _stream(stream)))
+
+
+# ---------------------------------------------------------------- e4m3 LM head
+
+def _dtype_of(t) -> int:
+    import torch
+    return {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}[t.dtype]
+
+
+def quantize_rows(x, x_out, scales, stream=None) -> None:
+    """x [R, H] fp32 or bf16 -> x_out [R, H] e4m3, scales [ceil(H / 128), R rounded up to 4]."""
+    R, H = x.shape
+    if tuple(x_out.shape) != (R, H) or tuple(scales.shape) != ((H + 127) // 128, (R + 3) // 4 * 4):
+        raise ValueError("x_out is [R, H] and scales [ceil(H / 128), R rounded up to 4]")
+    _check("eagle_quantize_rows", load().eagle_quantize_rows(
+        R, H, _dtype_of(x), _ptr(x), _ptr(x_out), _ptr(scales), _stream(stream)))
+
+
+def quantize_blocks(w, w_out, scales, stream=None) -> None:
+    """w [V, H] fp32 or bf16 -> w_out [V, H] e4m3, scales [ceil(V / 128), ceil(H / 128)]."""
+    V, H = w.shape
+    if tuple(w_out.shape) != (V, H) or tuple(scales.shape) != ((V + 127) // 128, (H + 127) // 128):
+        raise ValueError("w_out is [V, H] and scales [ceil(V / 128), ceil(H / 128)]")
+    _check("eagle_quantize_blocks", load().eagle_quantize_blocks(
+        V, H, _dtype_of(w), _ptr(w), _ptr(w_out), _ptr(scales), _stream(stream)))
+
+
+def lm_head_logits_scaled(x, x_scales, w, w_scales, logits, stream=None) -> None:
+    R, H = x.shape
+    V = w.shape[0]
+    KB = (H + 127) // 128
+    if (w.shape[1] != H or tuple(x_scales.shape) != (KB, (R + 3) // 4 * 4) or
+            tuple(w_scales.shape) != ((V + 127) // 128, KB) or tuple(logits.shape) != (R, V)):
+        raise ValueError("operands are x [R, H], x_scales [KB, R rounded up to 4], w [V, H], "
+                         "w_scales [ceil(V / 128), KB] and logits [R, V]")
+    _check("eagle_lm_head_logits_scaled", load().eagle_lm_head_logits_scaled(
+        R, H, V, _ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(logits), _stream(stream)))
 
 
 def device_error(reset: bool = True) -> int:

@@ -964,3 +964,5 @@ extern "C" eagle_status_t eagle_tree_attention_static(const eagle_shape_t* shape
   return run_attention(shape, q, k_prefix, v_prefix, prefix_lens, k_tree, v_tree, parents, out,
                        scratch, static_cast<cudaStream_t>(stream));
 }
+
+#include "paged_api.cuh"

@@ -1,0 +1,360 @@
+// paged_api.cuh -- C ABI of the paged-cache operators and of the e4m3 LM head (declared in
+// include/eagle_verify.h): argument checks, launch plans and launches.  Included by
+// eagle_verify.cu, whose helpers it uses.
+#pragma once
+
+#include "lm_head_scaled.cuh"
+#include "paged.cuh"
+#include "paged_attention.cuh"
+
+namespace eagle {
+namespace {
+
+// ------------------------------------------------------------------ checks
+
+eagle_status_t check_pages(const eagle_pages_t* pg) {
+  if (pg == nullptr) return EAGLE_ERR_INVALID_ARGUMENT;
+  if (pg->num_pages < 1 || pg->max_pages < 1) return EAGLE_ERR_INVALID_ARGUMENT;
+  const int32_t ps = pg->page_size;
+  if (ps < 16 || ps > 256 || (ps & (ps - 1)) != 0) return EAGLE_ERR_INVALID_ARGUMENT;
+  // positions are 32-bit
+  if (static_cast<int64_t>(pg->max_pages) * ps > INT32_MAX) return EAGLE_ERR_INVALID_ARGUMENT;
+  return EAGLE_OK;
+}
+
+PageMap page_map(const eagle_pages_t* pg, const int32_t* table) {
+  int shift = 4;
+  while ((1 << shift) < pg->page_size) ++shift;
+  return PageMap{table, pg->num_pages, shift, pg->max_pages};
+}
+
+eagle_status_t check_paged_shape(const eagle_shape_t* s, const eagle_pages_t* pg, int32_t shared_len) {
+  eagle_status_t rc = check_shape(s);
+  if (rc == EAGLE_OK) rc = check_pages(pg);
+  if (rc != EAGLE_OK) return rc;
+  if (static_cast<int64_t>(pg->max_pages) * pg->page_size < s->max_prefix_len) return EAGLE_ERR_INVALID_ARGUMENT;
+  if (shared_len < 0 || shared_len > s->max_prefix_len) return EAGLE_ERR_INVALID_ARGUMENT;
+  return EAGLE_OK;
+}
+
+// [a, a + an) and [b, b + bn) share a byte
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + bn && y < x + an;
+}
+
+int elem_size(const eagle_shape_t* s) { return s->dtype == EAGLE_DTYPE_BF16 ? 2 : 4; }
+
+// ------------------------------------------------------------------ append
+
+template <typename T, int D>
+void launch_append(const AppendParams& p, bool interleaved, int rows, cudaStream_t st) {
+  if (interleaved)
+    rope_append_kernel<T, D, true><<<rows, kAppendThreads, 0, st>>>(p);
+  else
+    rope_append_kernel<T, D, false><<<rows, kAppendThreads, 0, st>>>(p);
+}
+
+// A strided operand: 16-byte aligned rows that do not overlap one another, all of them
+// within 2^62 bytes.
+bool rows_ok(const void* x, int64_t stride, int64_t width, int esize, int64_t rows) {
+  return aligned16(x) && stride >= width && stride <= (static_cast<int64_t>(1) << 60) / rows &&
+         (stride * esize) % 16 == 0;
+}
+
+// A strided operand of `rows` rows and its bytes, first to last.
+struct RowSpan {
+  const void* p;
+  int64_t stride, width;
+  size_t bytes(int64_t rows, int esize) const {
+    return p == nullptr ? 0 : static_cast<size_t>(((rows - 1) * stride + width) * esize);
+  }
+};
+
+// A rotated output (dense) either is its own dense input or lies apart from every input.
+bool rotated_out_ok(const void* out, int64_t width, const RowSpan& own, const RowSpan (&in)[3], int64_t rows,
+                    int esize) {
+  if (out == own.p && own.stride != width) return false;
+  for (const RowSpan& x : in) {
+    if (x.p == nullptr || (x.p == own.p && out == own.p)) continue;
+    if (overlap(x.p, x.bytes(rows, esize), out, static_cast<size_t>(rows * width * esize))) return false;
+  }
+  return true;
+}
+
+// ------------------------------------------------------------------ attention
+
+template <typename T, int D>
+void launch_paged_simple(const void* q, const void* kp, const void* vp, const void* kt, const void* vt, void* out,
+                         const PagedAttnParams& p, cudaStream_t st) {
+  const int64_t rows = static_cast<int64_t>(p.B) * p.N * p.Hq;
+  tree_attn_paged_simple_kernel<T, D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(
+      static_cast<const T*>(q), static_cast<const T*>(kp), static_cast<const T*>(vp), static_cast<const T*>(kt),
+      static_cast<const T*>(vt), static_cast<T*>(out), p);
+}
+
+// ------------------------------------------------------------------ e4m3 LM head
+
+bool encode_bytes(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows) {
+  auto enc = get_encode();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {cols};
+  const cuuint32_t box[2] = {kScBlock, box_rows};
+  const cuuint32_t es[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int CW>
+eagle_status_t launch_scaled(const CUtensorMap& tw, const CUtensorMap& th, const ScaledParams& prm, dim3 grid,
+                             size_t smem, cudaStream_t st) {
+  // idempotent and cheap; set per call so that every device gets it
+  if (cudaFuncSetAttribute(lm_head_scaled_kernel<CW>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return EAGLE_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kScThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  // its set-up may overlap the end of the kernel before it (the quantiser); it waits for
+  // that kernel before it touches global memory
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, lm_head_scaled_kernel<CW>, tw, th, prm) != cudaSuccess) {
+    cudaGetLastError();
+    return EAGLE_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+bool dtype_ok(int32_t dtype) { return dtype == EAGLE_DTYPE_F32 || dtype == EAGLE_DTYPE_BF16; }
+
+}  // namespace
+}  // namespace eagle
+
+extern "C" {
+
+eagle_status_t eagle_rope_append(const eagle_shape_t* shape, const eagle_pages_t* pages, const eagle_rope_t* rope,
+                                 int32_t num_rows, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                 const void* v, int64_t v_stride, const int32_t* positions, const int32_t* seq_ids,
+                                 const float* cos_sin, void* k_pages, void* v_pages, const int32_t* page_table,
+                                 void* q_out, void* k_out, void* stream) {
+  eagle_status_t rc = check_shape(shape);
+  if (rc != EAGLE_OK) return rc;
+  if (rope == nullptr || num_rows < 0) return EAGLE_ERR_INVALID_ARGUMENT;
+  const int D = shape->head_dim, esize = elem_size(shape);
+  const int64_t qw = static_cast<int64_t>(shape->num_q_heads) * D, kw = static_cast<int64_t>(shape->num_kv_heads) * D;
+  if (qw > INT32_MAX || (rope->interleaved != 0 && rope->interleaved != 1)) return EAGLE_ERR_INVALID_ARGUMENT;
+  if (rope->rotary_dim < 0 || rope->rotary_dim > D || rope->rotary_dim % 16 != 0) return EAGLE_ERR_INVALID_ARGUMENT;
+  if (rope->rotary_dim > 0 && rope->table_len < 1) return EAGLE_ERR_INVALID_ARGUMENT;
+  if (num_rows == 0) return EAGLE_OK;
+  if (positions == nullptr || (rope->rotary_dim > 0 && !aligned16(cos_sin))) return EAGLE_ERR_INVALID_ARGUMENT;
+  const int64_t n = num_rows;
+  if ((q == nullptr) != (q_out == nullptr) || (q == nullptr && k == nullptr)) return EAGLE_ERR_INVALID_ARGUMENT;
+  if ((q != nullptr && (!rows_ok(q, q_stride, qw, esize, n) || !aligned16(q_out))) ||
+      (k != nullptr && !rows_ok(k, k_stride, kw, esize, n)) ||
+      (seq_ids != nullptr && (k == nullptr || v == nullptr || !rows_ok(v, v_stride, kw, esize, n))))
+    return EAGLE_ERR_INVALID_ARGUMENT;
+  const RowSpan in[3] = {{q, q_stride, qw}, {k, k_stride, kw}, {seq_ids != nullptr ? v : nullptr, v_stride, kw}};
+  if (q != nullptr && !rotated_out_ok(q_out, qw, in[0], in, n, esize)) return EAGLE_ERR_INVALID_ARGUMENT;
+  if (k_out != nullptr &&
+      (k == nullptr || !aligned16(k_out) || !rotated_out_ok(k_out, kw, in[1], in, n, esize) ||
+       (q != nullptr && overlap(q_out, static_cast<size_t>(n * qw * esize), k_out,
+                                static_cast<size_t>(n * kw * esize)))))
+    return EAGLE_ERR_INVALID_ARGUMENT;
+  AppendParams p{};
+  if (seq_ids != nullptr) {
+    rc = check_pages(pages);
+    if (rc != EAGLE_OK) return rc;
+    if (!aligned16(k_pages) || !aligned16(v_pages) || page_table == nullptr) return EAGLE_ERR_INVALID_ARGUMENT;
+    p.map = page_map(pages, page_table);
+  } else if (k != nullptr && k_out == nullptr) {
+    return EAGLE_ERR_INVALID_ARGUMENT;  // keys that go nowhere
+  }
+  p.q = static_cast<const uint8_t*>(q);
+  p.k = static_cast<const uint8_t*>(k);
+  p.v = static_cast<const uint8_t*>(v);
+  p.q_stride = q_stride * esize;
+  p.k_stride = k_stride * esize;
+  p.v_stride = v_stride * esize;
+  p.positions = positions;
+  p.seq_ids = seq_ids;
+  p.cos_sin = cos_sin;
+  p.k_pages = static_cast<uint8_t*>(k_pages);
+  p.v_pages = static_cast<uint8_t*>(v_pages);
+  p.q_out = static_cast<uint8_t*>(q_out);
+  p.k_out = static_cast<uint8_t*>(k_out);
+  p.B = shape->batch;
+  p.Hq = shape->num_q_heads;
+  p.Hkv = shape->num_kv_heads;
+  p.table_len = rope->table_len;
+  p.rd = rope->rotary_dim;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool il = rope->interleaved != 0;
+  if (shape->dtype == EAGLE_DTYPE_F32) {
+    D == 64 ? launch_append<float, 64>(p, il, num_rows, st) : launch_append<float, 128>(p, il, num_rows, st);
+  } else {
+    D == 64 ? launch_append<__nv_bfloat16, 64>(p, il, num_rows, st)
+            : launch_append<__nv_bfloat16, 128>(p, il, num_rows, st);
+  }
+  return launch_status();
+}
+
+size_t eagle_paged_workspace_bytes(const eagle_shape_t* shape, const eagle_pages_t* pages, int32_t shared_len) {
+  (void)shape;
+  (void)pages;
+  (void)shared_len;
+  return 0;
+}
+
+eagle_status_t eagle_tree_attention_paged(const eagle_shape_t* shape, const eagle_pages_t* pages, const void* q,
+                                          const void* k_pages, const void* v_pages, const int32_t* page_table,
+                                          const int32_t* prefix_lens, int32_t shared_len, const void* k_tree,
+                                          const void* v_tree, const int32_t* parents, void* out, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+  eagle_status_t rc = check_paged_shape(shape, pages, shared_len);
+  if (rc == EAGLE_OK)
+    rc = check_attention_args(shape, q, k_pages, v_pages, prefix_lens, k_tree, v_tree, parents, out, workspace,
+                              workspace_bytes, eagle_paged_workspace_bytes(shape, pages, shared_len));
+  if (rc != EAGLE_OK) return rc;
+  if (page_table == nullptr) return EAGLE_ERR_INVALID_ARGUMENT;
+  PagedAttnParams p{};
+  p.map = page_map(pages, page_table);
+  p.prefix_lens = prefix_lens;
+  p.parents = parents;
+  p.B = shape->batch;
+  p.N = shape->num_nodes;
+  p.Hq = shape->num_q_heads;
+  p.Hkv = shape->num_kv_heads;
+  p.G = p.Hq / p.Hkv;
+  p.Lmax = shape->max_prefix_len;
+  p.shared = shared_len;
+  p.scale = softmax_scale(shape);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool d64 = shape->head_dim == 64;
+  if (shape->dtype == EAGLE_DTYPE_F32) {
+    d64 ? launch_paged_simple<float, 64>(q, k_pages, v_pages, k_tree, v_tree, out, p, st)
+        : launch_paged_simple<float, 128>(q, k_pages, v_pages, k_tree, v_tree, out, p, st);
+  } else {
+    d64 ? launch_paged_simple<__nv_bfloat16, 64>(q, k_pages, v_pages, k_tree, v_tree, out, p, st)
+        : launch_paged_simple<__nv_bfloat16, 128>(q, k_pages, v_pages, k_tree, v_tree, out, p, st);
+  }
+  return launch_status();
+}
+
+eagle_status_t eagle_commit_accepted_paged(const eagle_shape_t* shape, const eagle_pages_t* pages, void* k_pages,
+                                           void* v_pages, const int32_t* page_table, const int32_t* prefix_lens,
+                                           const void* k_tree, const void* v_tree, const void* hidden,
+                                           const int32_t* parents, const int32_t* accepted_nodes,
+                                           const int32_t* accept_len, int32_t* new_prefix_lens, void* feat,
+                                           void* stream) {
+  eagle_status_t rc = check_commit_args(shape, k_pages, v_pages, prefix_lens, k_tree, v_tree, hidden, parents,
+                                        accepted_nodes, accept_len, new_prefix_lens, feat);
+  if (rc == EAGLE_OK) rc = check_pages(pages);
+  if (rc != EAGLE_OK) return rc;
+  if (page_table == nullptr) return EAGLE_ERR_INVALID_ARGUMENT;
+  const int esize = elem_size(shape);
+  CommitPagedParams p{};
+  p.k_pages = static_cast<uint8_t*>(k_pages);
+  p.v_pages = static_cast<uint8_t*>(v_pages);
+  p.map = page_map(pages, page_table);
+  p.prefix_lens = prefix_lens;
+  p.k_tree = static_cast<const uint8_t*>(k_tree);
+  p.v_tree = static_cast<const uint8_t*>(v_tree);
+  p.hidden = static_cast<const uint8_t*>(hidden);
+  p.parents = parents;
+  p.accepted_nodes = accepted_nodes;
+  p.accept_len = accept_len;
+  p.new_lens = new_prefix_lens;
+  p.feat = static_cast<uint8_t*>(feat);
+  p.N = shape->num_nodes;
+  p.Hkv = shape->num_kv_heads;
+  p.row_bytes = shape->head_dim * esize;
+  p.hrow_bytes = shape->hidden * esize;
+  const dim3 grid(shape->batch, shape->num_kv_heads + shape->num_nodes);
+  commit_paged_kernel<<<grid, kCommitThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  return launch_status();
+}
+
+eagle_status_t eagle_quantize_rows(int32_t rows, int32_t cols, int32_t dtype, const void* x, void* x_out,
+                                   float* scales, void* stream) {
+  if (rows < 0 || cols < 16 || cols % 16 != 0 || !dtype_ok(dtype)) return EAGLE_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return EAGLE_OK;
+  if (!aligned16(x) || !aligned16(x_out) || !aligned16(scales)) return EAGLE_ERR_INVALID_ARGUMENT;
+  if (rows > INT32_MAX - 3) return EAGLE_ERR_INVALID_ARGUMENT;
+  const int kblocks = (cols + kScBlock - 1) / kScBlock, ldm = (rows + 3) / 4 * 4;
+  const int64_t grid = (static_cast<int64_t>(rows) * kblocks + 3) / 4;
+  if (grid > INT32_MAX) return EAGLE_ERR_UNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == EAGLE_DTYPE_F32)
+    quantize_rows_kernel<float><<<static_cast<unsigned>(grid), 128, 0, st>>>(
+        static_cast<const float*>(x), static_cast<uint8_t*>(x_out), scales, rows, cols, kblocks, ldm);
+  else
+    quantize_rows_kernel<__nv_bfloat16><<<static_cast<unsigned>(grid), 128, 0, st>>>(
+        static_cast<const __nv_bfloat16*>(x), static_cast<uint8_t*>(x_out), scales, rows, cols, kblocks, ldm);
+  return launch_status();
+}
+
+eagle_status_t eagle_quantize_blocks(int32_t rows, int32_t cols, int32_t dtype, const void* w, void* w_out,
+                                     float* scales, void* stream) {
+  if (rows < 0 || cols < 16 || cols % 16 != 0 || !dtype_ok(dtype)) return EAGLE_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return EAGLE_OK;
+  if (!aligned16(w) || !aligned16(w_out) || scales == nullptr || (reinterpret_cast<uintptr_t>(scales) & 3) != 0)
+    return EAGLE_ERR_INVALID_ARGUMENT;
+  const int kblocks = (cols + kScBlock - 1) / kScBlock;
+  const int64_t grid = (static_cast<int64_t>(rows) + kScBlock - 1) / kScBlock * kblocks;
+  if (grid > INT32_MAX) return EAGLE_ERR_UNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == EAGLE_DTYPE_F32)
+    quantize_blocks_kernel<float><<<static_cast<unsigned>(grid), 256, 0, st>>>(
+        static_cast<const float*>(w), static_cast<uint8_t*>(w_out), scales, rows, cols, kblocks);
+  else
+    quantize_blocks_kernel<__nv_bfloat16><<<static_cast<unsigned>(grid), 256, 0, st>>>(
+        static_cast<const __nv_bfloat16*>(w), static_cast<uint8_t*>(w_out), scales, rows, cols, kblocks);
+  return launch_status();
+}
+
+eagle_status_t eagle_lm_head_logits_scaled(int32_t rows, int32_t hidden, int32_t vocab, const void* x,
+                                           const float* x_scales, const void* w, const float* w_scales,
+                                           float* logits, void* stream) {
+  if (rows < 0 || hidden < 16 || hidden % 16 != 0 || vocab < 1) return EAGLE_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return EAGLE_OK;
+  if (!aligned16(x) || !aligned16(x_scales) || !aligned16(w) || w_scales == nullptr ||
+      (reinterpret_cast<uintptr_t>(w_scales) & 3) != 0 || logits == nullptr ||
+      (reinterpret_cast<uintptr_t>(logits) & 3) != 0)
+    return EAGLE_ERR_INVALID_ARGUMENT;
+  const int64_t vtiles = (static_cast<int64_t>(vocab) + kScBlock - 1) / kScBlock;
+  if (rows > (1 << 24) || vtiles > 65535) return EAGLE_ERR_UNSUPPORTED;
+  // rows in equal chunks of at most 256 (the MMA's largest N)
+  int chunks = (rows + 255) / 256;
+  const int bn = ((rows + chunks - 1) / chunks + 15) / 16 * 16;
+  chunks = (rows + bn - 1) / bn;
+  CUtensorMap tw, th;
+  if (!encode_bytes(&tw, w, static_cast<uint64_t>(hidden), static_cast<uint64_t>(vocab), kScBlock) ||
+      !encode_bytes(&th, x, static_cast<uint64_t>(hidden), static_cast<uint64_t>(rows), static_cast<uint32_t>(bn)))
+    return EAGLE_ERR_CUDA;
+  int stages = 2;
+  // two CTAs per SM up to 128 rows, else one with the deepest ring
+  const size_t budget = bn <= 128 ? 110 * 1024 : 220 * 1024;
+  while (stages < 8 && scaled_smem_bytes(bn, stages + 1) <= budget) ++stages;
+  const int KB = (hidden + kScBlock - 1) / kScBlock;
+  ScaledParams prm{logits, x_scales, w_scales, rows, vocab, hidden, KB, (rows + 3) / 4 * 4, bn, stages};
+  const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(vtiles));
+  const size_t smem = scaled_smem_bytes(bn, stages);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (bn <= 16) return launch_scaled<8>(tw, th, prm, grid, smem, st);
+  if (bn <= 32) return launch_scaled<16>(tw, th, prm, grid, smem, st);
+  if (bn <= 64) return launch_scaled<32>(tw, th, prm, grid, smem, st);
+  if (bn <= 128) return launch_scaled<64>(tw, th, prm, grid, smem, st);
+  return launch_scaled<128>(tw, th, prm, grid, smem, st);
+}
+
+}  // extern "C"
