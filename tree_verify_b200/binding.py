@@ -135,12 +135,8 @@ def workspace_bytes(shape: Shape) -> int:
 # ---------------------------------------------------------------- tensor marshalling
 
 def _ptr(t) -> Optional[int]:
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or type(t) is int:
         return t
-    import torch
-    assert isinstance(t, torch.Tensor)
     if not t.is_cuda:
         raise ValueError("library arguments are device tensors")
     if not t.is_contiguous():
@@ -148,11 +144,22 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_current_stream = None
+
+
 def _stream(stream) -> Optional[int]:
+    global _current_stream
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    if _current_stream is None:
+        import torch
+        torch.cuda.current_stream()  # (initialises CUDA)
+        raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        if raw is not None and device is not None:  # the same handle without a Stream object around it
+            _current_stream = lambda: raw(device())
+        else:
+            _current_stream = lambda: torch.cuda.current_stream().cuda_stream
+    return _current_stream()
 
 
 def _check(fn: str, code: int) -> None:
@@ -246,16 +253,17 @@ def _rows(t):
         return None, 0
     if not t.is_cuda:
         raise ValueError("library arguments are device tensors")
-    if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+    rows, heads, d = t.shape
+    stride, head, one = t.stride()
+    if one != 1 or head != d:
         raise ValueError("token rows are [R, heads, D] with dense heads")
-    R, heads, d = t.shape
-    return t.data_ptr(), (t.stride(0) if R > 1 else heads * d)
+    return t.data_ptr(), (stride if rows > 1 else heads * d)
 
 
 def rope_append(shape: Shape, pages: Optional[Pages], q, k, v, positions, seq_ids, cos_sin, k_pages,
                 v_pages, page_table, q_out, k_out=None, interleaved: bool = False, stream=None) -> None:
     """cos_sin [table_len, rotary_dim], or None for rotary_dim 0; seq_ids None: rotation only."""
-    rope = Rope(0, 0, 0) if cos_sin is None else Rope(cos_sin.shape[0], cos_sin.shape[1], int(interleaved))
+    rope = Rope(0, 0, 0) if cos_sin is None else Rope(*cos_sin.shape, interleaved)
     qp, qs = _rows(q)
     kp, ks = _rows(k)
     vp, vs = _rows(v)
@@ -289,9 +297,14 @@ def commit_accepted_paged(shape: Shape, pages: Pages, k_pages, v_pages, page_tab
 
 # ---------------------------------------------------------------- e4m3 LM head
 
+_DTYPES = {}
+
+
 def _dtype_of(t) -> int:
-    import torch
-    return {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}[t.dtype]
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16})
+    return _DTYPES[t.dtype]
 
 
 def quantize_rows(x, x_out, scales, stream=None) -> None:

@@ -6,6 +6,7 @@
 #include "lm_head_scaled.cuh"
 #include "paged.cuh"
 #include "paged_attention.cuh"
+#include "paged_attention_tc.cuh"
 
 namespace eagle {
 namespace {
@@ -84,13 +85,125 @@ bool rotated_out_ok(const void* out, int64_t width, const RowSpan& own, const Ro
 
 // ------------------------------------------------------------------ attention
 
-template <typename T, int D>
-void launch_paged_simple(const void* q, const void* kp, const void* vp, const void* kt, const void* vt, void* out,
-                         const PagedAttnParams& p, cudaStream_t st) {
+template <int D>
+void launch_paged_f32(const void* q, const void* kp, const void* vp, const void* kt, const void* vt, void* out,
+                      const PagedAttnParams& p, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(p.B) * p.N * p.Hq;
-  tree_attn_paged_simple_kernel<T, D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(
-      static_cast<const T*>(q), static_cast<const T*>(kp), static_cast<const T*>(vp), static_cast<const T*>(kt),
-      static_cast<const T*>(vt), static_cast<T*>(out), p);
+  tree_attn_paged_simple_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(
+      static_cast<const float*>(q), static_cast<const float*>(kp), static_cast<const float*>(vp),
+      static_cast<const float*>(kt), static_cast<const float*>(vt), static_cast<float*>(out), p);
+}
+
+// Row tiles and partials of the tensor-core form, from what the host knows: the lengths may
+// be anything up to Lmax, so every item may be cut, and each has a run more than it is cut.
+struct PagedPlan {
+  int nodes_per_tile, rb_own, rb_sh, rows_own, rows_sh;
+  int64_t own_row0, part_rows;
+  size_t plan_bytes, ml_bytes, acc_bytes;
+  size_t bytes() const { return plan_bytes + ml_bytes + acc_bytes; }
+};
+
+PagedPlan plan_paged(const eagle_shape_t* s, int32_t shared_len) {
+  PagedPlan p{};
+  const int G = s->num_q_heads / s->num_kv_heads;
+  const int64_t B = s->batch, N = s->num_nodes, Hkv = s->num_kv_heads;
+  const int nb = G <= kTcRows ? kTcRows / G : 1;
+  p.nodes_per_tile = nb;
+  p.rb_own = static_cast<int>((N + nb - 1) / nb);
+  p.rb_sh = shared_len > 0 ? static_cast<int>((B * N + nb - 1) / nb) : 0;
+  p.rows_own = static_cast<int>(N < nb ? N : nb) * G;
+  p.rows_sh = static_cast<int>(B * N < nb ? B * N : nb) * G;
+  p.own_row0 = shared_len > 0 ? 2 * (Hkv * ((p.rb_sh + 1) / 2) + kNumSMs) * p.rows_sh : 0;
+  p.part_rows = p.own_row0 + 2 * (B * Hkv * ((p.rb_own + 1) / 2) + kNumSMs) * p.rows_own;
+  p.plan_bytes = align256(static_cast<size_t>(2 + B) * sizeof(int64_t));
+  p.ml_bytes = align256(static_cast<size_t>(p.part_rows) * sizeof(float2));
+  p.acc_bytes = align256(static_cast<size_t>(p.part_rows) * s->head_dim * sizeof(float));
+  return p;
+}
+
+template <int D>
+bool paged_attributes() {
+  // idempotent and cheap; set per call so that every device gets it
+  if (cudaFuncSetAttribute(paged_attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           PgSmem<D>::kAlloc) == cudaSuccess) {
+    // the softmax groups' larger share of registers comes out of what the block was launched
+    // with: never launch a build whose total falls short of the shares
+    static const bool enough = [] {
+      cudaFuncAttributes a{};
+      return cudaFuncGetAttributes(&a, paged_attn_tc_kernel<D>) == cudaSuccess &&
+             a.numRegs * kPgThreads >= 256 * kPgSoftRegs + 128 * kPgOtherRegs;
+    }();
+    return enough;
+  }
+  cudaGetLastError();
+  return false;
+}
+
+template <int D>
+eagle_status_t launch_paged_tc(const eagle_shape_t* s, const eagle_pages_t* pg, const PagedAttnParams& ap,
+                               const void* q, const void* kp, const void* vp, const void* kt, const void* vt,
+                               void* out, void* ws, cudaStream_t st) {
+  if (!paged_attributes<D>()) return EAGLE_ERR_CUDA;
+  const PagedPlan plan = plan_paged(s, ap.shared);
+  PagedTcParams p{};
+  p.a = ap;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  p.plan = reinterpret_cast<int64_t*>(w);
+  p.part_ml = reinterpret_cast<float2*>(w + plan.plan_bytes);
+  p.part_acc = reinterpret_cast<float*>(w + plan.plan_bytes + plan.ml_bytes);
+  p.NB = plan.nodes_per_tile;
+  p.rb_own = plan.rb_own;
+  p.rb_sh = plan.rb_sh;
+  p.rows_own = plan.rows_own;
+  p.rows_sh = plan.rows_sh;
+  p.own_row0 = plan.own_row0;
+  p.box = pg->page_size < kAttnKeys ? pg->page_size : kAttnKeys;
+  p.ctas = kNumSMs;
+  p.scale_log2 = ap.scale * 1.4426950408889634f;
+  CUtensorMap tq, tk, tv, tkt, tvt;
+  using u64 = cuuint64_t;
+  const u64 Dn = D, Hq = ap.Hq, Hkv = ap.Hkv, N = ap.N, B = ap.B, ps = pg->page_size;
+  // pages viewed as [num_pages][Hkv][page_size][D]: a box is `box` rows of one page and head
+  const u64 kdims[4] = {Dn, ps, Hkv, static_cast<u64>(pg->num_pages)};
+  const u64 kstrides[3] = {Dn * 2, ps * Dn * 2, Hkv * ps * Dn * 2};
+  const cuuint32_t kbox[4] = {64, static_cast<cuuint32_t>(p.box), 1, 1};
+  // queries viewed as [B * N, Hq, D]: a box is NB nodes x the G heads of a kv head
+  const u64 qdims[3] = {Dn, Hq, B * N};
+  const u64 qstrides[2] = {Dn * 2, Hq * Dn * 2};
+  const cuuint32_t qbox[3] = {64, static_cast<cuuint32_t>(ap.G), static_cast<cuuint32_t>(p.NB)};
+  // tree K/V viewed as [B][N][Hkv][D]: a box is the node rows of (b, kv head), zeros past N
+  const u64 tdims[4] = {Dn, Hkv, N, B};
+  const u64 tstrides[3] = {Dn * 2, Hkv * Dn * 2, N * Hkv * Dn * 2};
+  const cuuint32_t tbox[4] = {64, 1, static_cast<cuuint32_t>(kAttnKeys), 1};
+  if (!encode_bf16(&tk, kp, 4, kdims, kstrides, kbox) || !encode_bf16(&tv, vp, 4, kdims, kstrides, kbox) ||
+      !encode_bf16(&tq, q, 3, qdims, qstrides, qbox) || !encode_bf16(&tkt, kt, 4, tdims, tstrides, tbox) ||
+      !encode_bf16(&tvt, vt, 4, tdims, tstrides, tbox))
+    return EAGLE_ERR_CUDA;
+  paged_attn_tc_kernel<D><<<kNumSMs, kPgThreads, PgSmem<D>::kAlloc, st>>>(tq, tk, tv, tkt, tvt, p);
+  const eagle_status_t rc = launch_status();
+  if (rc != EAGLE_OK) return rc;
+  // the merge may be launched while the kernel above runs, and waits for it; eight warps
+  // share a row's partials while that does not make more than a few CTAs per SM
+  const int64_t rows = static_cast<int64_t>(ap.B) * ap.N * ap.Hq;
+  const bool split = (rows + 7) / 8 * (D / 16) <= 4 * kNumSMs;
+  const int per = split ? kPgMergeRows<true> : kPgMergeRows<false>;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + per - 1) / per), split ? D / 16 : 1);
+  cfg.blockDim = dim3(split ? 256 : 2 * D);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = split ? cudaLaunchKernelEx(&cfg, paged_attn_merge_kernel<D, true>, p)
+                              : cudaLaunchKernelEx(&cfg, paged_attn_merge_kernel<D, false>, p);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return EAGLE_ERR_CUDA;
+  }
+  return launch_status();
 }
 
 // ------------------------------------------------------------------ e4m3 LM head
@@ -209,10 +322,9 @@ eagle_status_t eagle_rope_append(const eagle_shape_t* shape, const eagle_pages_t
 }
 
 size_t eagle_paged_workspace_bytes(const eagle_shape_t* shape, const eagle_pages_t* pages, int32_t shared_len) {
-  (void)shape;
-  (void)pages;
-  (void)shared_len;
-  return 0;
+  if (check_paged_shape(shape, pages, shared_len) != EAGLE_OK) return 0;
+  if (shape->dtype != EAGLE_DTYPE_BF16) return 0;
+  return plan_paged(shape, shared_len).bytes();
 }
 
 eagle_status_t eagle_tree_attention_paged(const eagle_shape_t* shape, const eagle_pages_t* pages, const void* q,
@@ -241,11 +353,11 @@ eagle_status_t eagle_tree_attention_paged(const eagle_shape_t* shape, const eagl
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool d64 = shape->head_dim == 64;
   if (shape->dtype == EAGLE_DTYPE_F32) {
-    d64 ? launch_paged_simple<float, 64>(q, k_pages, v_pages, k_tree, v_tree, out, p, st)
-        : launch_paged_simple<float, 128>(q, k_pages, v_pages, k_tree, v_tree, out, p, st);
+    d64 ? launch_paged_f32<64>(q, k_pages, v_pages, k_tree, v_tree, out, p, st)
+        : launch_paged_f32<128>(q, k_pages, v_pages, k_tree, v_tree, out, p, st);
   } else {
-    d64 ? launch_paged_simple<__nv_bfloat16, 64>(q, k_pages, v_pages, k_tree, v_tree, out, p, st)
-        : launch_paged_simple<__nv_bfloat16, 128>(q, k_pages, v_pages, k_tree, v_tree, out, p, st);
+    return d64 ? launch_paged_tc<64>(shape, pages, p, q, k_pages, v_pages, k_tree, v_tree, out, workspace, st)
+               : launch_paged_tc<128>(shape, pages, p, q, k_pages, v_pages, k_tree, v_tree, out, workspace, st);
   }
   return launch_status();
 }

@@ -13,23 +13,13 @@ struct PagedAttnParams {
   float scale;
 };
 
-template <typename T>
-__device__ __forceinline__ float elem_f32(T x);
-template <>
-__device__ __forceinline__ float elem_f32<float>(float x) {
-  return x;
-}
-template <>
-__device__ __forceinline__ float elem_f32<__nv_bfloat16>(__nv_bfloat16 x) {
-  return __bfloat162float(x);
-}
-
-// One warp per output row: 32 keys at a time, one per lane for the scores, then D / 32
+// fp32: one warp per output row: 32 keys at a time, one per lane for the scores, then D / 32
 // output columns per lane.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(128)
-    tree_attn_paged_simple_kernel(const T* __restrict__ q, const T* __restrict__ kp, const T* __restrict__ vp,
-                                  const T* __restrict__ kt, const T* __restrict__ vt, T* __restrict__ out,
+    tree_attn_paged_simple_kernel(const float* __restrict__ q, const float* __restrict__ kp,
+                                  const float* __restrict__ vp, const float* __restrict__ kt,
+                                  const float* __restrict__ vt, float* __restrict__ out,
                                   const PagedAttnParams p) {
   __shared__ float q_s[4][D];
   __shared__ int path_s[4][64];
@@ -44,7 +34,7 @@ __global__ void __launch_bounds__(128)
   float acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) {
-    q_s[wid][lane + 32 * e] = elem_f32(q[row * D + lane + 32 * e]);
+    q_s[wid][lane + 32 * e] = q[row * D + lane + 32 * e];
     acc[e] = 0.f;
   }
   int np = 0;
@@ -61,7 +51,7 @@ __global__ void __launch_bounds__(128)
   int L = p.prefix_lens[b];
   if ((L < 0 || L > p.Lmax) && lane == 0) record_error(kErrAttnPrefixLen);
   L = L < 0 ? 0 : (L > p.Lmax ? p.Lmax : L);
-  auto key_row = [&](int j, const T* pool, const T* tree) -> const T* {
+  auto key_row = [&](int j, const float* pool, const float* tree) -> const float* {
     if (j >= L) return tree + ((static_cast<size_t>(b) * p.N + path_s[wid][j - L]) * p.Hkv + g) * D;
     const int32_t pg = page_of(p.map, b, j);
     return pg < 0 ? nullptr : pool + page_row(p.map, pg, g, p.Hkv, j, D);
@@ -72,10 +62,10 @@ __global__ void __launch_bounds__(128)
     const int j = c + lane;
     float s = -INFINITY;
     if (j < nk) {
-      const T* kr = key_row(j, kp, kt);
+      const float* kr = key_row(j, kp, kt);
       float dot = 0.f;
       if (kr != nullptr)
-        for (int d = 0; d < D; ++d) dot = fmaf(q_s[wid][d], elem_f32(kr[d]), dot);
+        for (int d = 0; d < D; ++d) dot = fmaf(q_s[wid][d], kr[d], dot);
       s = dot * p.scale;
     }
     float cm = s;
@@ -92,23 +82,18 @@ __global__ void __launch_bounds__(128)
     for (int e = 0; e < kPer; ++e) acc[e] *= corr;
     const int cnt = min(32, nk - c);
     for (int t = 0; t < cnt; ++t) {
-      const T* vr = key_row(c + t, vp, vt);
+      const float* vr = key_row(c + t, vp, vt);
       const float pt = __shfl_sync(0xffffffffu, pr, t);
       if (vr != nullptr) {
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(pt, elem_f32(vr[lane + 32 * e]), acc[e]);
+        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(pt, vr[lane + 32 * e], acc[e]);
       }
     }
     m = mn;
   }
   const float inv = 1.0f / l;
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    if constexpr (sizeof(T) == 4)
-      out[row * D + lane + 32 * e] = acc[e] * inv;
-    else
-      out[row * D + lane + 32 * e] = __float2bfloat16_rn(acc[e] * inv);
-  }
+  for (int e = 0; e < kPer; ++e) out[row * D + lane + 32 * e] = acc[e] * inv;
 }
 
 }  // namespace eagle
