@@ -196,6 +196,18 @@ __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, 
       : "memory");
 }
 
+// True in one lane of a converged warp.  The compiler knows that a branch on it leaves one
+// thread, so the operands that tcgen05 instructions take from uniform registers need no
+// search for the lanes that share a value.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 // Arrive once on `bar` when every tcgen05 op issued so far by this thread has completed.
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -314,6 +326,18 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int m, int n) {
 // Same with B MN-major (bit 16).
 __host__ __device__ constexpr uint32_t idesc_bf16_f32_bmn(int m, int n) {
   return idesc_bf16_f32(m, n) | (1u << 16);
+}
+
+// Moves registers between groups of four warps of a CTA: the shares after every reg_inc and
+// reg_dec must not add up to more than the CTA was launched with, or the reg_inc waits for
+// ever (register_shares_fit, checked on the host).
+template <int R>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
 // ------------------------------------------------------------------ clusters

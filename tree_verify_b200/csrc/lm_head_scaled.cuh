@@ -7,12 +7,13 @@
 // them in fp32 (measured against fp64: relative error 1.3e-8 on normal data, as an fp32 FMA
 // chain); the blocks are scaled and summed in fp32 registers.
 //
-// The GEMM is swap-AB like lm_head.cuh: 128 vocabulary rows are the MMA's M, the few tree
-// rows its N, so the weight streams once.  A vocabulary tile is one row of scale blocks, so
-// every K block of a tile has a single ws.  Per K block one 128-deep MMA chain goes into a
-// fresh TMEM buffer; two groups of four epilogue warps (thread = vocabulary row, group =
-// half of the tree rows) scale it into their register accumulators while the next block's
-// MMAs run.
+// Two forms, by the number of tree rows (each measured at both sizes, see the kernels):
+//   up to 64 rows    swap-AB like lm_head.cuh: 128 vocabulary rows are the MMA's M, the tree
+//                    rows its N; the weight streams once and bounds it;
+//   more             tree rows as M (128 a tile), one or two blocks of 128 vocabulary rows
+//                    as N, so that a thread's accumulators all share one scale.
+// In both, per K block one 128-deep MMA chain goes into a fresh TMEM buffer and eight
+// epilogue warps scale it into their register accumulators while the next blocks' MMAs run.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -24,6 +25,7 @@ namespace eagle {
 constexpr int kScBlock = 128;        // elements that share a scale; vocabulary rows per CTA
 constexpr int kScThreads = 32 * 10;  // TMA, MMA, 8 epilogue warps
 constexpr int kScEpiWarps = 8;
+constexpr int kScFewRows = 32;       // rows up to which the weight is the MMA's M
 
 // 2^e and 2^-e for the smallest e >= -126 with amax <= 448 * 2^e: amax = m * 2^k with
 // 1 <= m < 2, and 448 = 1.75 * 2^8, so e = k - 8 while m <= 1.75 and k - 7 above.  The
@@ -145,42 +147,37 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int m, int n) {
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
-// Untiled bulk copy (addresses and size multiples of 16 bytes).
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
 struct ScaledParams {
   float* logits;
   const float* hs;  // [KB, ldm]
   const float* ws;  // [ceil(V / 128), KB]
   int32_t M, V, H, KB, ldm;
-  int32_t bn;       // tree rows per CTA (MMA N): a multiple of 16, <= 2 * CW
-  int32_t stages;
+  int32_t bn;       // few rows: rows rounded up to 16; many: row tiles
+  int32_t stages;   // few rows: slots of the ring; many: vocabulary tiles
+  int32_t vec;      // many rows: rows of logits are 16-byte aligned
 };
 
-constexpr uint32_t kScW = kScBlock * kScBlock;  // bytes of a W tile
-constexpr uint32_t kScHs = 1024;                // bytes of a stage's row scales (256 rows)
+constexpr uint32_t kScTile = kScBlock * kScBlock;  // bytes of 128 rows of a K block
+
+// ------------------------------------------------------------------ few rows
+
 __host__ __device__ inline uint32_t scaled_stage_bytes(int bn) {
-  return kScW + static_cast<uint32_t>(bn) * kScBlock + kScHs;
+  return kScTile + static_cast<uint32_t>(bn) * kScBlock;
 }
 __host__ __device__ inline size_t scaled_smem_bytes(int bn, int stages) {
   return 1024 + static_cast<size_t>(stages) * scaled_stage_bytes(bn) + (2 * stages + 9) * 8 + 16;
 }
 
-// CW: accumulator columns (tree rows) of an epilogue thread.
+// CW: accumulator columns (tree rows) of an epilogue thread: 8, 16 or 32.
 template <int CW>
 struct ScaledCfg {
-  // TMEM columns of a buffer (tcgen05.alloc takes powers of two from 32), and buffers:
-  // four while two CTAs of an SM fit their 512 columns together
+  // TMEM columns of a buffer (tcgen05.alloc takes powers of two from 32), and buffers: two
+  // CTAs of an SM fit their 512 columns together
   static constexpr int kCols = 2 * CW < 32 ? 32 : 2 * CW;
-  static constexpr int kBufs = CW <= 32 ? 4 : 2;
-  static constexpr int kStep = CW < 16 ? CW : 16;  // columns per TMEM load
+  static constexpr int kBufs = 4;
 };
 
+__device__ __forceinline__ void tmem_ld_step(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_32x32b_x32(taddr, r); }
 __device__ __forceinline__ void tmem_ld_step(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_32x32b_x16(taddr, r); }
 __device__ __forceinline__ void tmem_ld_step(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -189,7 +186,7 @@ __device__ __forceinline__ void tmem_ld_step(uint32_t taddr, uint32_t (&r)[8]) {
 }
 
 template <int CW>
-__global__ void __launch_bounds__(kScThreads)
+__global__ void __launch_bounds__(kScThreads, 2)
     lm_head_scaled_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_h,
                           const ScaledParams prm) {
   using C = ScaledCfg<CW>;
@@ -198,9 +195,8 @@ __global__ void __launch_bounds__(kScThreads)
                                              ~static_cast<uintptr_t>(1023));
   const int S = prm.stages, bn = prm.bn, KB = prm.KB;
   uint8_t* w_tiles = smem;
-  uint8_t* h_tiles = w_tiles + S * kScW;
-  uint8_t* hs_tiles = h_tiles + S * bn * kScBlock;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(hs_tiles + S * kScHs);
+  uint8_t* h_tiles = w_tiles + S * kScTile;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(h_tiles + S * bn * kScBlock);
   uint64_t* full = bars;
   uint64_t* empty = full + S;
   uint64_t* acc_full = empty + S;
@@ -209,15 +205,14 @@ __global__ void __launch_bounds__(kScThreads)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r0 = blockIdx.x * bn;
-  const int vb = blockIdx.y, v0 = vb * kScBlock;
+  const int vb = blockIdx.x, v0 = vb * kScBlock;
 
   if (threadIdx.x == 0) {
     prefetch_tmap(&tm_w);
     prefetch_tmap(&tm_h);
     for (int s = 0; s < S; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), 1 + kScEpiWarps);  // the MMAs and the readers of the scales
+      mbar_init(smem_u32(&empty[s]), 1);
     }
     for (int u = 0; u < C::kBufs; ++u) {
       mbar_init(smem_u32(&acc_full[u]), 1);
@@ -239,8 +234,7 @@ __global__ void __launch_bounds__(kScThreads)
   if (warp == 0) {
     if (lane == 0) {
       // ---------------- TMA producer
-      const int hs_rows = min(bn, prm.ldm - r0);
-      const uint32_t bytes = kScW + static_cast<uint32_t>(bn) * kScBlock + static_cast<uint32_t>(hs_rows) * 4;
+      const uint32_t bytes = scaled_stage_bytes(bn);
       const uint64_t pol_w = l2_policy_evict_first();
       const uint64_t pol_h = l2_policy_evict_last();
       int issued = 0;
@@ -249,10 +243,8 @@ __global__ void __launch_bounds__(kScThreads)
         if (n > 0 && !mbar_wait(smem_u32(&empty[s]), (n - 1) & 1, kErrLmProducerWait)) break;
         const uint32_t fb = smem_u32(&full[s]);
         mbar_arrive_expect_tx(fb, bytes);
-        tma_load_2d_hint(smem_u32(w_tiles + s * kScW), &tm_w, fb, kb * kScBlock, v0, pol_w);
-        tma_load_2d_hint(smem_u32(h_tiles + s * bn * kScBlock), &tm_h, fb, kb * kScBlock, r0, pol_h);
-        bulk_load(smem_u32(hs_tiles + s * kScHs), prm.hs + static_cast<size_t>(kb) * prm.ldm + r0,
-                  static_cast<uint32_t>(hs_rows) * 4, fb);
+        tma_load_2d_hint(smem_u32(w_tiles + s * kScTile), &tm_w, fb, kb * kScBlock, v0, pol_w);
+        tma_load_2d_hint(smem_u32(h_tiles + s * bn * kScBlock), &tm_h, fb, kb * kScBlock, 0, pol_h);
         issued = kb + 1;
       }
       // every issued load lands before this CTA's shared memory can be released
@@ -260,7 +252,7 @@ __global__ void __launch_bounds__(kScThreads)
         mbar_wait(smem_u32(&full[kb % S]), (kb / S) & 1, kErrLmProducerWait);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ---------------- MMA issuer
       const uint32_t idesc = idesc_e4m3_f32(kScBlock, bn);
       for (int kb = 0; kb < KB; ++kb) {
@@ -270,7 +262,7 @@ __global__ void __launch_bounds__(kScThreads)
         ok = ok && mbar_wait(smem_u32(&full[s]), (kb / S) & 1, kErrLmMmaWait);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t a = smem_desc_k_sw128(smem_u32(w_tiles + s * kScW));
+        const uint64_t a = smem_desc_k_sw128(smem_u32(w_tiles + s * kScTile));
         const uint64_t b = smem_desc_k_sw128(smem_u32(h_tiles + s * bn * kScBlock));
 #pragma unroll
         for (int k = 0; k < kScBlock / 32; ++k)
@@ -291,51 +283,49 @@ __global__ void __launch_bounds__(kScThreads)
     const int v = v0 + quarter * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(col0);
     const float* wsv = prm.ws + static_cast<size_t>(vb) * KB;
+    // the row scales come through L1 (every lane reads the same ones); columns past the
+    // last row take the scales of rows that exist, for sums that are not stored
+    const int last4 = prm.ldm / 4 - 1;
+    const bool any = col0 < prm.M;
     float2 acc[CW / 2];
 #pragma unroll
     for (int j = 0; j < CW / 2; ++j) acc[j] = make_float2(0.f, 0.f);
     float w_next = wsv[0];
     bool ok = true;
-    for (int kb = 0; kb < KB && ok; ++kb) {
-      const int s = kb % S, u = kb % C::kBufs;
+    for (int kb = 0; kb < KB; ++kb) {
+      const int u = kb % C::kBufs;
       const float w = w_next;
       if (kb + 1 < KB) w_next = wsv[kb + 1];
-      ok = mbar_wait(smem_u32(&full[s]), (kb / S) & 1, kErrLmEpilogueWait) &&
-           mbar_wait(smem_u32(&acc_full[u]), (kb / C::kBufs) & 1, kErrLmEpilogueWait);
+      const float4* hs = reinterpret_cast<const float4*>(prm.hs + static_cast<size_t>(kb) * prm.ldm);
+      ok = ok && mbar_wait(smem_u32(&acc_full[u]), (kb / C::kBufs) & 1, kErrLmEpilogueWait);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      const float4* hs = reinterpret_cast<const float4*>(hs_tiles + s * kScHs) + col0 / 4;
-#pragma unroll
-      for (int c = 0; c < CW; c += C::kStep) {
-        if (col0 + c >= bn) continue;  // uniform over the warp
-        uint32_t d[C::kStep];
-        tmem_ld_step(lane_base + static_cast<uint32_t>(u * C::kCols + c), d);
+      uint32_t d[CW];
+      if (any) {
+        tmem_ld_step(lane_base + static_cast<uint32_t>(u * C::kCols), d);
         tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < C::kStep; j += 4) {
-          const float4 h4 = hs[(c + j) / 4];
-          const float2 s0 = fmul2(make_float2(h4.x, h4.y), make_float2(w, w));
-          const float2 s1 = fmul2(make_float2(h4.z, h4.w), make_float2(w, w));
-          acc[(c + j) / 2] =
-              ffma2(make_float2(__uint_as_float(d[j]), __uint_as_float(d[j + 1])), s0, acc[(c + j) / 2]);
-          acc[(c + j) / 2 + 1] =
-              ffma2(make_float2(__uint_as_float(d[j + 2]), __uint_as_float(d[j + 3])), s1, acc[(c + j) / 2 + 1]);
-        }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&acc_empty[u]));
-        mbar_arrive(smem_u32(&empty[s]));
+      if (lane == 0) mbar_arrive(smem_u32(&acc_empty[u]));
+      if (any) {
+#pragma unroll
+        for (int j = 0; j < CW / 4; ++j) {
+          const float4 h4 = __ldg(hs + min(col0 / 4 + j, last4));
+          const float2 s0 = fmul2(make_float2(h4.x, h4.y), make_float2(w, w));
+          const float2 s1 = fmul2(make_float2(h4.z, h4.w), make_float2(w, w));
+          acc[2 * j] = ffma2(make_float2(__uint_as_float(d[4 * j]), __uint_as_float(d[4 * j + 1])), s0, acc[2 * j]);
+          acc[2 * j + 1] =
+              ffma2(make_float2(__uint_as_float(d[4 * j + 2]), __uint_as_float(d[4 * j + 3])), s1, acc[2 * j + 1]);
+        }
       }
     }
     if (ok && v < prm.V) {
 #pragma unroll
       for (int j = 0; j < CW; ++j) {
-        const int row = r0 + col0 + j;
-        if (col0 + j < bn && row < prm.M)
-          prm.logits[static_cast<size_t>(row) * prm.V + v] = (j & 1) ? acc[j / 2].y : acc[j / 2].x;
+        if (col0 + j < prm.M)
+          prm.logits[static_cast<size_t>(col0 + j) * prm.V + v] = (j & 1) ? acc[j / 2].y : acc[j / 2].x;
       }
     }
   }
@@ -344,6 +334,257 @@ __global__ void __launch_bounds__(kScThreads)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols * C::kBufs);
+  }
+}
+
+// ------------------------------------------------------------------ many rows
+// One CTA per SM walks the (vocabulary tile, row tile) pairs, row tiles fastest, so CTAs
+// that need the same weight tile run side by side and it comes from HBM once.  A thread owns
+// one tree row and half of the tile's columns: its scale is one number per K block (row
+// scale x block scale), and nothing of the epilogue goes through shared memory, where per K
+// block and two vocabulary blocks TMA writes 48 KB and the MMAs read 48 KB in 512 MMA
+// clocks.  The logits leave through a 2 KB patch per warp, so that whole sectors are written
+// (each thread writing its own row instead: 360 us against 318 on 512 rows of 128256 x 4096).
+// That case runs at about 1,080 clocks per K block at 1.6 GHz under the power cap: 160 are
+// the stores, 590 the MMAs and their operands alone, the rest the hand-offs of the two TMEM
+// buffers.  Sixteen epilogue warps with a quarter of the columns each took the same time
+// (321 us), swap-AB with 256 tree rows as N 747.
+
+// Warps 0-7 epilogue, 8 TMA, 9 MMA; 10 and 11 only complete a group of four, which is what
+// registers are moved between.
+constexpr int kScRowsThreads = 32 * 12;
+constexpr int kScRowsTmaWarp = 8, kScRowsMmaWarp = 9;
+constexpr int kScRowsEpiRegs = 208, kScRowsOtherRegs = 88;  // of the launch's 168 x 384 registers
+
+template <int NV>
+struct ScaledRowsCfg {
+  static constexpr int kN = kScBlock * NV;          // vocabulary rows of a tile
+  static constexpr int kCW = kN / 2;                // accumulators of a thread
+  static constexpr int kStage = kScTile * (1 + NV);
+  static constexpr int kStages = NV == 2 ? 4 : 6;
+  static constexpr int kBufs = 512 / kN;            // all of TMEM
+  static constexpr int kPatch = 32 * 64;            // a warp's 32 rows x 16 columns
+  static constexpr int kPatchOff = kStages * kStage;
+  static constexpr int kBarOff = kPatchOff + kScEpiWarps * kPatch;
+  static constexpr int kBytes = kBarOff + (2 * kStages + 2 * kBufs + 1) * 8 + 16;
+  static constexpr int kAlloc = kBytes + 1024;
+  static_assert(kAlloc <= 227 * 1024, "shared memory");
+};
+
+template <int NV>
+__global__ void __launch_bounds__(kScRowsThreads, 1)
+    lm_head_scaled_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_h,
+                               const ScaledParams prm) {
+  using C = ScaledRowsCfg<NV>;
+  constexpr int S = C::kStages, kBufs = C::kBufs, CW = C::kCW;
+  extern __shared__ uint8_t scr_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(scr_smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t full = sbase + C::kBarOff, empty = full + 8 * S, acc_full = empty + 8 * S;
+  const uint32_t acc_empty = acc_full + 8 * kBufs, mma_done = acc_empty + 8 * kBufs;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + (2 * S + 2 * kBufs + 1) * 8);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int KB = prm.KB, row_tiles = prm.bn;
+  const int64_t tiles = static_cast<int64_t>(prm.stages) * row_tiles;
+
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&tm_w);
+    prefetch_tmap(&tm_h);
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, 1);
+    }
+    for (int u = 0; u < kBufs; ++u) {
+      mbar_init(acc_full + 8 * u, 1);
+      mbar_init(acc_empty + 8 * u, kScEpiWarps);
+    }
+    mbar_init(mma_done, 1);
+    fence_mbar_init();
+  }
+  if (warp == kScRowsMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+
+  // (registers: the epilogue of two blocks holds 128 sums a thread)
+  if (warp >= kScEpiWarps) {
+    if constexpr (NV == 2) reg_dec<kScRowsOtherRegs>();
+    if (warp == kScRowsTmaWarp && elect_one()) {
+      // ---------------- TMA producer
+      const uint64_t pol_w = row_tiles > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+      const uint64_t pol_h = l2_policy_evict_last();
+      int s = 0;
+      int64_t issued = 0;
+      uint32_t phase = 1;  // parity of the slot's last release; the first round waits for none
+      bool ok = true;
+      for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        const int vt = static_cast<int>(t / row_tiles), rt = static_cast<int>(t % row_tiles);
+        for (int kb = 0; kb < KB; ++kb) {
+          if (issued >= S && !mbar_wait(empty + 8 * s, phase, kErrLmProducerWait)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = full + 8 * s, dst = sbase + s * C::kStage;
+          mbar_arrive_expect_tx(fb, C::kStage);
+          tma_load_2d_hint(dst, &tm_h, fb, kb * kScBlock, rt * kScBlock, pol_h);
+#pragma unroll
+          for (int b = 0; b < NV; ++b)
+            tma_load_2d_hint(dst + (1 + b) * kScTile, &tm_w, fb, kb * kScBlock, (vt * NV + b) * kScBlock, pol_w);
+          ++issued;
+          if (++s == S) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // every issued load lands before this CTA's shared memory can be released
+      for (int64_t i = issued > S ? issued - S : 0; i < issued; ++i)
+        mbar_wait(full + 8 * static_cast<int>(i % S), static_cast<uint32_t>(i / S) & 1, kErrLmProducerWait);
+    }
+    if (warp == kScRowsMmaWarp && elect_one()) {
+      // ---------------- MMA issuer
+      constexpr uint32_t idesc = idesc_e4m3_f32(kScBlock, C::kN);
+      int s = 0, u = 0;
+      uint32_t ph = 0, pu = 1;
+      int64_t n = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int kb = 0; kb < KB; ++kb) {
+          ok = (n < kBufs || mbar_wait(acc_empty + 8 * u, pu, kErrLmMmaWait)) &&
+               mbar_wait(full + 8 * s, ph, kErrLmMmaWait);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t a = smem_desc_k_sw128(sbase + s * C::kStage);
+          const uint64_t b = smem_desc_k_sw128(sbase + s * C::kStage + kScTile);
+#pragma unroll
+          for (int k = 0; k < kScBlock / 32; ++k)
+            tc_mma_f8(tmem + static_cast<uint32_t>(u * C::kN), a + 2 * k, b + 2 * k, idesc, k > 0 ? 1u : 0u);
+          tc_commit(empty + 8 * s);
+          tc_commit(acc_full + 8 * u);
+          ++n;
+          if (++s == S) {
+            s = 0;
+            ph ^= 1;
+          }
+          if (++u == kBufs) {
+            u = 0;
+            pu ^= 1;
+          }
+        }
+      }
+      // orders the TMEM release after every MMA issued
+      tc_commit(mma_done);
+      mbar_wait(mma_done, 0, kErrLmMmaWait);
+    }
+    __syncwarp();
+  } else {
+    if constexpr (NV == 2) reg_inc<kScRowsEpiRegs>();
+    // ---------------- epilogue
+    const int quarter = warp & 3;         // TMEM lanes this warp may access
+    const int grp = warp >> 2;            // half of the tile's columns
+    const uint32_t lane_base =
+        tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(grp * CW);
+    float* patch = reinterpret_cast<float*>(smem + C::kPatchOff + warp * C::kPatch);
+    int u = 0;
+    uint32_t pu = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const int vt = static_cast<int>(t / row_tiles), rt = static_cast<int>(t % row_tiles);
+      const int row0 = rt * kScBlock + quarter * 32;      // the warp's first row
+      const int col0 = vt * C::kN + grp * CW;             // ... and column
+      const bool any = row0 < prm.M && col0 < prm.V;
+      const float* wsv = prm.ws + static_cast<size_t>(any ? col0 / kScBlock : 0) * KB;
+      const float* hsv = prm.hs + min(row0 + lane, prm.M - 1);
+      float2 acc[CW / 2];
+#pragma unroll
+      for (int j = 0; j < CW / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+      // scales are loaded three blocks ahead (about an L2 round trip)
+      float w1 = __ldg(wsv), h1 = __ldg(hsv), w2 = 0.f, h2 = 0.f, w3 = 0.f, h3 = 0.f;
+      if (KB > 1) {
+        w2 = __ldg(wsv + 1);
+        h2 = __ldg(hsv + prm.ldm);
+      }
+      if (KB > 2) {
+        w3 = __ldg(wsv + 2);
+        h3 = __ldg(hsv + 2 * static_cast<size_t>(prm.ldm));
+      }
+      for (int kb = 0; kb < KB; ++kb) {
+        const float sc = w1 * h1;
+        w1 = w2;
+        h1 = h2;
+        w2 = w3;
+        h2 = h3;
+        if (kb + 3 < KB) {
+          w3 = __ldg(wsv + kb + 3);
+          h3 = __ldg(hsv + static_cast<size_t>(kb + 3) * prm.ldm);
+        }
+        ok = ok && mbar_wait(acc_full + 8 * u, pu, kErrLmEpilogueWait);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (any) {
+          const uint32_t at = lane_base + static_cast<uint32_t>(u * C::kN);
+          const float2 s2 = make_float2(sc, sc);
+#pragma unroll
+          for (int c = 0; c < CW; c += 16) {
+            uint32_t d[16];
+            tmem_ld_cols<16>(at + c, d);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              acc[c / 2 + j] =
+                  ffma2(make_float2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1])), s2, acc[c / 2 + j]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty + 8 * u);
+        if (++u == kBufs) {
+          u = 0;
+          pu ^= 1;
+        }
+      }
+      if (!ok || !any) continue;
+      // 16 columns at a time: thread = row into the patch (16-byte chunks, index XOR row / 2),
+      // then 4 threads a row out of it
+#pragma unroll
+      for (int c = 0; c < CW; c += 16) {
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          reinterpret_cast<float4*>(patch)[lane * 4 + (q ^ ((lane >> 1) & 3))] =
+              make_float4(acc[c / 2 + 2 * q].x, acc[c / 2 + 2 * q].y, acc[c / 2 + 2 * q + 1].x, acc[c / 2 + 2 * q + 1].y);
+        __syncwarp();
+        const int q = lane & 3, col = col0 + c + 4 * q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 8 + (lane >> 2);
+          const float4 x = reinterpret_cast<const float4*>(patch)[r * 4 + (q ^ ((r >> 1) & 3))];
+          if (row0 + r >= prm.M) continue;
+          float* dst = prm.logits + static_cast<size_t>(row0 + r) * prm.V + col;
+          if (prm.vec) {
+            if (col < prm.V) *reinterpret_cast<float4*>(dst) = x;  // V is a multiple of 4
+          } else {
+            if (col < prm.V) dst[0] = x.x;
+            if (col + 1 < prm.V) dst[1] = x.y;
+            if (col + 2 < prm.V) dst[2] = x.z;
+            if (col + 3 < prm.V) dst[3] = x.w;
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kScRowsMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 

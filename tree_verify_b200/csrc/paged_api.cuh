@@ -46,6 +46,29 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
 
 int elem_size(const eagle_shape_t* s) { return s->dtype == EAGLE_DTYPE_BF16 ? 2 : 4; }
 
+// ------------------------------------------------------------------ kernel attributes
+
+// Idempotent and cheap: set per call, so that every device gets it.
+template <typename K>
+bool allow_smem(K kernel, int bytes) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
+// Kernels whose first warps take `inc` registers a thread out of what the CTA was launched
+// with, the last four keeping `dec`: a build that was launched with fewer would wait for
+// ever, so it is never launched.
+template <typename K>
+bool register_shares_fit(K kernel, int threads, int inc, int dec) {
+  cudaFuncAttributes a{};
+  if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return a.numRegs * threads >= (threads - 128) * inc + 128 * dec;
+}
+
 // ------------------------------------------------------------------ append
 
 template <typename T, int D>
@@ -85,13 +108,72 @@ bool rotated_out_ok(const void* out, int64_t width, const RowSpan& own, const Ro
 
 // ------------------------------------------------------------------ attention
 
-template <int D>
-void launch_paged_f32(const void* q, const void* kp, const void* vp, const void* kt, const void* vt, void* out,
-                      const PagedAttnParams& p, cudaStream_t st) {
-  const int64_t rows = static_cast<int64_t>(p.B) * p.N * p.Hq;
-  tree_attn_paged_simple_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(
-      static_cast<const float*>(q), static_cast<const float*>(kp), static_cast<const float*>(vp),
-      static_cast<const float*>(kt), static_cast<const float*>(vt), static_cast<float*>(out), p);
+// The fp32 form: row tiles of 16 rows where no more are in a sequence's kv head, else 64;
+// key tiles divided so that there are about three CTAs for each SM.
+struct PagedF32Plan {
+  int rt, splits, tiles_own, tiles_sh;
+  int64_t items;
+  size_t ml_bytes, acc_bytes;
+  bool direct() const { return splits == 1 && tiles_sh == 0; }
+  size_t bytes() const { return direct() ? 0 : ml_bytes + acc_bytes; }
+};
+
+PagedF32Plan plan_paged_f32(const eagle_shape_t* s, int32_t shared_len) {
+  PagedF32Plan p{};
+  const int64_t G = s->num_q_heads / s->num_kv_heads, B = s->batch, N = s->num_nodes, Hkv = s->num_kv_heads;
+  p.rt = N * G <= 16 ? 16 : 64;
+  p.tiles_own = static_cast<int>((N * G + p.rt - 1) / p.rt);
+  p.tiles_sh = shared_len > 0 ? static_cast<int>((B * N * G + p.rt - 1) / p.rt) : 0;
+  p.items = Hkv * (B * p.tiles_own + p.tiles_sh);
+  const int kt = s->head_dim == 128 ? PagedF32Cfg<128, 64>::kKT : PagedF32Cfg<64, 64>::kKT;
+  const int64_t tiles = (static_cast<int64_t>(s->max_prefix_len) + kt - 1) / kt + (N + kt - 1) / kt;
+  int64_t splits = (3 * kNumSMs + p.items - 1) / p.items;
+  if (splits > tiles) splits = tiles;
+  p.splits = static_cast<int>(splits);
+  const size_t rows = static_cast<size_t>(p.items) * p.splits * p.rt;
+  p.ml_bytes = align256(rows * sizeof(float2));
+  p.acc_bytes = align256(rows * s->head_dim * sizeof(float));
+  return p;
+}
+
+template <int D, int RT>
+eagle_status_t launch_paged_f32(const PagedF32Plan& plan, const void* q, const void* kp, const void* vp,
+                                const void* kt, const void* vt, void* out, void* ws, const PagedAttnParams& ap,
+                                cudaStream_t st) {
+  constexpr int bytes = PagedF32Cfg<D, RT>::kBytes;
+  if (!allow_smem(paged_attn_f32_kernel<D, RT>, bytes)) return EAGLE_ERR_CUDA;
+  PagedF32Params p{};
+  p.a = ap;
+  p.q = static_cast<const float*>(q);
+  p.kp = static_cast<const float*>(kp);
+  p.vp = static_cast<const float*>(vp);
+  p.kt = static_cast<const float*>(kt);
+  p.vt = static_cast<const float*>(vt);
+  p.out = static_cast<float*>(out);
+  p.part_ml = static_cast<float2*>(ws);
+  p.part_acc = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + plan.ml_bytes);
+  p.splits = plan.splits;
+  p.tiles_own = plan.tiles_own;
+  p.tiles_sh = plan.tiles_sh;
+  p.direct = plan.direct();
+  paged_attn_f32_kernel<D, RT><<<dim3(static_cast<unsigned>(plan.items), plan.splits), 128, bytes, st>>>(p);
+  const eagle_status_t rc = launch_status();
+  if (rc != EAGLE_OK || p.direct) return rc;
+  const int64_t threads = static_cast<int64_t>(ap.B) * ap.N * ap.Hq * (D / 4);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((threads + 127) / 128));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, paged_attn_f32_merge_kernel<D, RT>, p) != cudaSuccess) {
+    cudaGetLastError();
+    return EAGLE_ERR_CUDA;
+  }
+  return launch_status();
 }
 
 // Row tiles and partials of the tensor-core form, from what the host knows: the lengths may
@@ -122,28 +204,11 @@ PagedPlan plan_paged(const eagle_shape_t* s, int32_t shared_len) {
 }
 
 template <int D>
-bool paged_attributes() {
-  // idempotent and cheap; set per call so that every device gets it
-  if (cudaFuncSetAttribute(paged_attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           PgSmem<D>::kAlloc) == cudaSuccess) {
-    // the softmax groups' larger share of registers comes out of what the block was launched
-    // with: never launch a build whose total falls short of the shares
-    static const bool enough = [] {
-      cudaFuncAttributes a{};
-      return cudaFuncGetAttributes(&a, paged_attn_tc_kernel<D>) == cudaSuccess &&
-             a.numRegs * kPgThreads >= 256 * kPgSoftRegs + 128 * kPgOtherRegs;
-    }();
-    return enough;
-  }
-  cudaGetLastError();
-  return false;
-}
-
-template <int D>
 eagle_status_t launch_paged_tc(const eagle_shape_t* s, const eagle_pages_t* pg, const PagedAttnParams& ap,
                                const void* q, const void* kp, const void* vp, const void* kt, const void* vt,
                                void* out, void* ws, cudaStream_t st) {
-  if (!paged_attributes<D>()) return EAGLE_ERR_CUDA;
+  static const bool shares = register_shares_fit(paged_attn_tc_kernel<D>, kPgThreads, kPgSoftRegs, kPgOtherRegs);
+  if (!shares || !allow_smem(paged_attn_tc_kernel<D>, PgSmem<D>::kAlloc)) return EAGLE_ERR_CUDA;
   const PagedPlan plan = plan_paged(s, ap.shared);
   PagedTcParams p{};
   p.a = ap;
@@ -220,18 +285,13 @@ bool encode_bytes(CUtensorMap* map, const void* base, uint64_t cols, uint64_t ro
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CW>
-eagle_status_t launch_scaled(const CUtensorMap& tw, const CUtensorMap& th, const ScaledParams& prm, dim3 grid,
-                             size_t smem, cudaStream_t st) {
-  // idempotent and cheap; set per call so that every device gets it
-  if (cudaFuncSetAttribute(lm_head_scaled_kernel<CW>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
-      cudaSuccess) {
-    cudaGetLastError();
-    return EAGLE_ERR_CUDA;
-  }
+template <typename K>
+eagle_status_t launch_scaled(K kernel, const CUtensorMap& tw, const CUtensorMap& th, const ScaledParams& prm,
+                             unsigned grid, unsigned threads, size_t smem, cudaStream_t st) {
+  if (!allow_smem(kernel, 227 * 1024)) return EAGLE_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kScThreads);
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   // its set-up may overlap the end of the kernel before it (the quantiser); it waits for
@@ -241,7 +301,7 @@ eagle_status_t launch_scaled(const CUtensorMap& tw, const CUtensorMap& th, const
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, lm_head_scaled_kernel<CW>, tw, th, prm) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kernel, tw, th, prm) != cudaSuccess) {
     cudaGetLastError();
     return EAGLE_ERR_CUDA;
   }
@@ -323,8 +383,8 @@ eagle_status_t eagle_rope_append(const eagle_shape_t* shape, const eagle_pages_t
 
 size_t eagle_paged_workspace_bytes(const eagle_shape_t* shape, const eagle_pages_t* pages, int32_t shared_len) {
   if (check_paged_shape(shape, pages, shared_len) != EAGLE_OK) return 0;
-  if (shape->dtype != EAGLE_DTYPE_BF16) return 0;
-  return plan_paged(shape, shared_len).bytes();
+  return shape->dtype == EAGLE_DTYPE_BF16 ? plan_paged(shape, shared_len).bytes()
+                                          : plan_paged_f32(shape, shared_len).bytes();
 }
 
 eagle_status_t eagle_tree_attention_paged(const eagle_shape_t* shape, const eagle_pages_t* pages, const void* q,
@@ -352,14 +412,16 @@ eagle_status_t eagle_tree_attention_paged(const eagle_shape_t* shape, const eagl
   p.scale = softmax_scale(shape);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool d64 = shape->head_dim == 64;
-  if (shape->dtype == EAGLE_DTYPE_F32) {
-    d64 ? launch_paged_f32<64>(q, k_pages, v_pages, k_tree, v_tree, out, p, st)
-        : launch_paged_f32<128>(q, k_pages, v_pages, k_tree, v_tree, out, p, st);
-  } else {
+  if (shape->dtype == EAGLE_DTYPE_BF16)
     return d64 ? launch_paged_tc<64>(shape, pages, p, q, k_pages, v_pages, k_tree, v_tree, out, workspace, st)
                : launch_paged_tc<128>(shape, pages, p, q, k_pages, v_pages, k_tree, v_tree, out, workspace, st);
-  }
-  return launch_status();
+  const PagedF32Plan plan = plan_paged_f32(shape, shared_len);
+  if (plan.items > INT32_MAX) return EAGLE_ERR_UNSUPPORTED;
+  if (plan.rt == 16)
+    return d64 ? launch_paged_f32<64, 16>(plan, q, k_pages, v_pages, k_tree, v_tree, out, workspace, p, st)
+               : launch_paged_f32<128, 16>(plan, q, k_pages, v_pages, k_tree, v_tree, out, workspace, p, st);
+  return d64 ? launch_paged_f32<64, 64>(plan, q, k_pages, v_pages, k_tree, v_tree, out, workspace, p, st)
+             : launch_paged_f32<128, 64>(plan, q, k_pages, v_pages, k_tree, v_tree, out, workspace, p, st);
 }
 
 eagle_status_t eagle_commit_accepted_paged(const eagle_shape_t* shape, const eagle_pages_t* pages, void* k_pages,
@@ -445,28 +507,45 @@ eagle_status_t eagle_lm_head_logits_scaled(int32_t rows, int32_t hidden, int32_t
     return EAGLE_ERR_INVALID_ARGUMENT;
   const int64_t vtiles = (static_cast<int64_t>(vocab) + kScBlock - 1) / kScBlock;
   if (rows > (1 << 24) || vtiles > 65535) return EAGLE_ERR_UNSUPPORTED;
-  // rows in equal chunks of at most 256 (the MMA's largest N)
-  int chunks = (rows + 255) / 256;
-  const int bn = ((rows + chunks - 1) / chunks + 15) / 16 * 16;
-  chunks = (rows + bn - 1) / bn;
+  const int KB = (hidden + kScBlock - 1) / kScBlock;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   CUtensorMap tw, th;
+  ScaledParams prm{logits, x_scales, w_scales, rows, vocab, hidden, KB, (rows + 3) / 4 * 4, 0, 0, 0};
+  const bool few = rows <= kScFewRows;
+  const int bn = few ? (rows + 15) / 16 * 16 : kScBlock;
   if (!encode_bytes(&tw, w, static_cast<uint64_t>(hidden), static_cast<uint64_t>(vocab), kScBlock) ||
       !encode_bytes(&th, x, static_cast<uint64_t>(hidden), static_cast<uint64_t>(rows), static_cast<uint32_t>(bn)))
     return EAGLE_ERR_CUDA;
-  int stages = 2;
-  // two CTAs per SM up to 128 rows, else one with the deepest ring
-  const size_t budget = bn <= 128 ? 110 * 1024 : 220 * 1024;
-  while (stages < 8 && scaled_smem_bytes(bn, stages + 1) <= budget) ++stages;
-  const int KB = (hidden + kScBlock - 1) / kScBlock;
-  ScaledParams prm{logits, x_scales, w_scales, rows, vocab, hidden, KB, (rows + 3) / 4 * 4, bn, stages};
-  const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(vtiles));
-  const size_t smem = scaled_smem_bytes(bn, stages);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (bn <= 16) return launch_scaled<8>(tw, th, prm, grid, smem, st);
-  if (bn <= 32) return launch_scaled<16>(tw, th, prm, grid, smem, st);
-  if (bn <= 64) return launch_scaled<32>(tw, th, prm, grid, smem, st);
-  if (bn <= 128) return launch_scaled<64>(tw, th, prm, grid, smem, st);
-  return launch_scaled<128>(tw, th, prm, grid, smem, st);
+  if (few) {
+    // two CTAs per SM, each with as deep a ring as fits
+    int stages = 2;
+    while (stages < 8 && scaled_smem_bytes(bn, stages + 1) <= 113 * 1024) ++stages;
+    prm.bn = bn;
+    prm.stages = stages;
+    const size_t smem = scaled_smem_bytes(bn, stages);
+    const unsigned grid = static_cast<unsigned>(vtiles);
+    if (bn <= 16) return launch_scaled(lm_head_scaled_kernel<8>, tw, th, prm, grid, kScThreads, smem, st);
+    if (bn <= 32) return launch_scaled(lm_head_scaled_kernel<16>, tw, th, prm, grid, kScThreads, smem, st);
+    return launch_scaled(lm_head_scaled_kernel<32>, tw, th, prm, grid, kScThreads, smem, st);
+  }
+  // two vocabulary blocks a tile (two thirds of the shared-memory bytes per product) while
+  // there are six of them per SM, so that the last round of tiles is a small part
+  const int row_tiles = (rows + kScBlock - 1) / kScBlock;
+  const int64_t wide = (vtiles + 1) / 2 * row_tiles;
+  const int nv = wide >= 6 * kNumSMs ? 2 : 1;
+  prm.bn = row_tiles;
+  prm.stages = static_cast<int32_t>((vtiles + nv - 1) / nv);
+  prm.vec = vocab % 4 == 0 && aligned16(logits);
+  const int64_t tiles = static_cast<int64_t>(prm.stages) * row_tiles;
+  const unsigned grid = static_cast<unsigned>(tiles < kNumSMs ? tiles : kNumSMs);
+  if (nv == 2) {
+    static const bool shares =
+        register_shares_fit(lm_head_scaled_rows_kernel<2>, kScRowsThreads, kScRowsEpiRegs, kScRowsOtherRegs);
+    if (!shares) return EAGLE_ERR_CUDA;
+    return launch_scaled(lm_head_scaled_rows_kernel<2>, tw, th, prm, grid, kScRowsThreads, ScaledRowsCfg<2>::kAlloc,
+                         st);
+  }
+  return launch_scaled(lm_head_scaled_rows_kernel<1>, tw, th, prm, grid, kScRowsThreads, ScaledRowsCfg<1>::kAlloc, st);
 }
 
 }  // extern "C"

@@ -197,27 +197,6 @@ struct PgSmem {
   static_assert(kScanOff % 8 == 0 && kBarOff % 8 == 0, "alignment");
 };
 
-// True in one lane of a converged warp.  The compiler knows that a branch on it leaves one
-// thread, so the operands that tcgen05 instructions take from uniform registers need no
-// search for the lanes that share a value.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-template <int R>
-__device__ __forceinline__ void reg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
-template <int R>
-__device__ __forceinline__ void reg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
-}
-
 template <int D>
 __global__ void __launch_bounds__(kPgThreads, 1)
     paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
