@@ -230,6 +230,24 @@ def test_attention_repeats_bit_for_bit_on_streams_and_in_graphs(cuda_lib, dtype)
     assert torch.equal(out, first)
 
 
+def test_attention_ragged_batch_repeats(cuda_lib):
+    """Short sequences of every length, so that runs of single tiles follow one another on a
+    CTA: the same bits every time, with other memory traffic in between."""
+    c = _case(33003, *ATTN[-1], "bf16")
+    _, out, call, guards = _launcher(cuda_lib, c)
+    call()
+    guards()
+    _check(c, out)
+    first = out.clone()
+    junk = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    for i in range(60):
+        out.fill_(7.0)
+        if i % 3 == 0:
+            junk.fill_(i)
+        call()
+        assert torch.equal(out, first), i
+
+
 def test_attention_two_calls_at_once(cuda_lib):
     """Two calls on two streams, each with its own workspace."""
     a = _case(11, 3, 30, 8, 2, 128, 16, 64, [2000, 64, 700], "bf16")

@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     }
     for (int s = 0; s < SK; ++s) {
       mbar_init(k_full + 8 * s, 1);
-      mbar_init(k_empty + 8 * s, 2);  // either group, or one of them twice
+      mbar_init(k_empty + 8 * s, 2);  // either group
     }
     for (int s = 0; s < SV; ++s) {
       mbar_init(v_full + 8 * s, 1);
@@ -514,16 +514,29 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           return true;
         }
       };
+      // Waits for the K tile of gi.  On the way it sees the other group's tiles land and gives
+      // up its claim to their slots: every phase of a slot's barrier is seen by both issuers,
+      // and no slot is filled again before, since a wait for a phase is only sound while the
+      // barrier is not more than that phase ahead or behind.
+      int seen = 0;
+      auto reach = [&]() {
+        for (; seen < gi && ok; ++seen) {
+          wait(k_full + 8 * (seen % SK), (seen / SK) & 1);
+          if (ok) mbar_arrive(k_empty + 8 * (seen % SK));
+          wait(v_full + 8 * (seen % SV), (seen / SV) & 1);
+          if (ok) mbar_arrive(v_empty + 8 * (seen % SV));
+        }
+        wait(k_full + 8 * (gi % SK), (gi / SK) & 1);
+      };
       // (a test of a barrier takes some 300 clocks while the tensor core reads shared memory:
       // those for operands are made under the MMAs issued before)
       bool more = open(), first = true;
       if (more) {
         wait(qf, 0);
-        wait(k_full + 8 * (gi % SK), (gi / SK) & 1);
+        reach();
       }
       while (more && ok) {
         const int sk = gi % SK, sv = gi % SV;
-        const bool twice = step == 2;  // the other group does not read this tile
         tc_fence_after();
         const uint64_t ad = smem_desc_k_sw128(qb), bd = smem_desc_k_sw128(sbase + SM::kKOff + sk * SM::kTile);
 #pragma unroll
@@ -533,8 +546,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         }
         tc_commit(sf);
         tc_commit(k_empty + 8 * sk);
-        if (twice) tc_commit(k_empty + 8 * sk);
         wait(v_full + 8 * sv, (gi / SV) & 1);
+        seen = gi + 1;
         const uint64_t vd = smem_desc_mn_sw128(sbase + SM::kVOff + sv * SM::kTile, kAttnKeys * 128, 1024);
         wait(ph, n & 1);
         if (!ok) break;
@@ -550,7 +563,6 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           tc_mma_f16_ts(o_tmem, s_tmem + 8 * kk, vd + kk * (2048 / 16), idesc_o, 1u);
         tc_commit(pd);
         tc_commit(v_empty + 8 * sv);
-        if (twice) tc_commit(v_empty + 8 * sv);
         first = false;
         gi += step;
         if (gi >= end) {
@@ -559,7 +571,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           more = open();
           if (more) wait(qf, (q - 1) & 1);
         }
-        if (more) wait(k_full + 8 * (gi % SK), (gi / SK) & 1);
+        if (more) reach();
         wait(pd, n & 1);
         ++n;
       }
@@ -609,9 +621,13 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         const bool tree = t == tree_t;
         const int pos = t0 + t * kAttnKeys;
         const int valid = tree ? N : min(kAttnKeys, L - pos);
+        wait(s_full + 8 * g, n & 1);
+        tc_fence_after();
         if (!tree && valid < kAttnKeys) {
           // what the last page holds past the length must not reach P V, whatever it is:
-          // zero those rows of the V slot once it has landed (later boxes came in as zeros)
+          // zero those rows of the V slot once it has landed (later boxes came in as zeros).
+          // The slot's tile before this one has landed -- the issuer saw it before this S --
+          // so the wait cannot take its phase for that one's.
           const int gi = base + t - a, s = gi % SV;
           wait(v_full + 8 * s, (gi / SV) & 1);
           const int end = (valid + prm.box - 1) & ~(prm.box - 1);
@@ -621,9 +637,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vb + attn_swz(j, dd)), "r"(0) : "memory");
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();  // lane 0's arrivals below speak for the whole warp
         }
-        wait(s_full + 8 * g, n & 1);
-        tc_fence_after();
         if (live) {
           float x[kAttnKeys];
           __syncwarp();  // the TMEM loads below are warp-wide
