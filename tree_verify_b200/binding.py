@@ -1,8 +1,11 @@
-"""ctypes binding of libeagle_verify.so (the C ABI in include/eagle_verify.h).
+"""Binding of libeagle_verify.so (the C ABI in include/eagle_verify.h).
 
 Argument marshalling only: torch tensors become device pointers and the current CUDA
 stream becomes the `stream` argument; every step of the computation runs in the
-library's kernels.  There is no fallback: if the library is missing, ``load()`` raises.
+library's kernels.  The calls of the verification step go through ctypes, those of the
+paged cache and the e4m3 LM head, which a server makes for every layer or token, through a
+small CPython module (csrc/marshal.cpp).  There is no fallback: if either is missing, the
+call raises.
 """
 from __future__ import annotations
 
@@ -12,6 +15,7 @@ from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libeagle_verify.so")
+MARSHAL_PATH = os.path.join(PKG, "_marshal.so")
 
 EAGLE_OK = 0
 EAGLE_ERR_INVALID_ARGUMENT = 1
@@ -246,31 +250,37 @@ def draft_child_rows(probs, tokens, child_probs, stream=None) -> None:
 
 # ---------------------------------------------------------------- paged cache
 
-def _rows(t):
-    """(pointer, row stride in elements) of a [R, heads, D] tensor whose rows may be strided
-    parts of a wider array."""
-    if t is None:
-        return None, 0
-    if not t.is_cuda:
-        raise ValueError("library arguments are device tensors")
-    rows, heads, d = t.shape
-    stride, head, one = t.stride()
-    if one != 1 or head != d:
-        raise ValueError("token rows are [R, heads, D] with dense heads")
-    return t.data_ptr(), (stride if rows > 1 else heads * d)
+_module = None
+
+
+def _native():
+    """The marshalling module (csrc/marshal.cpp), bound to the library's entry points."""
+    global _module
+    if _module is None:
+        if not os.path.exists(MARSHAL_PATH):
+            raise RuntimeError(f"marshalling module not built: {MARSHAL_PATH} is missing "
+                               "(run `python -m tree_verify_b200.build`)")
+        import importlib.util
+
+        import torch  # noqa: F401  (the module links to it)
+        lib = load()
+        spec = importlib.util.spec_from_file_location("tree_verify_b200._marshal", MARSHAL_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(ctypes.cast(getattr(lib, "eagle_" + name), ctypes.c_void_p).value for name in
+                      ("rope_append", "tree_attention_paged", "commit_accepted_paged", "quantize_rows",
+                       "quantize_blocks", "lm_head_logits_scaled")))
+        _module = module
+    return _module
 
 
 def rope_append(shape: Shape, pages: Optional[Pages], q, k, v, positions, seq_ids, cos_sin, k_pages,
                 v_pages, page_table, q_out, k_out=None, interleaved: bool = False, stream=None) -> None:
-    """cos_sin [table_len, rotary_dim], or None for rotary_dim 0; seq_ids None: rotation only."""
-    rope = Rope(0, 0, 0) if cos_sin is None else Rope(*cos_sin.shape, interleaved)
-    qp, qs = _rows(q)
-    kp, ks = _rows(k)
-    vp, vs = _rows(v)
-    _check("eagle_rope_append", load().eagle_rope_append(
-        ctypes.byref(shape), None if pages is None else ctypes.byref(pages), ctypes.byref(rope),
-        positions.shape[0], qp, qs, kp, ks, vp, vs, _ptr(positions), _ptr(seq_ids), _ptr(cos_sin),
-        _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(q_out), _ptr(k_out), _stream(stream)))
+    """cos_sin [table_len, rotary_dim], or None for rotary_dim 0; seq_ids None: rotation only.  q, k
+    and v may be strided parts of a packed projection."""
+    _check("eagle_rope_append", (_module or _native()).rope_append(
+        shape, pages, q, k, v, positions, seq_ids, cos_sin, k_pages, v_pages, page_table, q_out, k_out, interleaved,
+        stream))
 
 
 def paged_workspace_bytes(shape: Shape, pages: Pages, shared_len: int) -> int:
@@ -280,61 +290,36 @@ def paged_workspace_bytes(shape: Shape, pages: Pages, shared_len: int) -> int:
 def tree_attention_paged(shape: Shape, pages: Pages, q, k_pages, v_pages, page_table, prefix_lens,
                          shared_len: int, k_tree, v_tree, parents, out, workspace=None,
                          stream=None) -> None:
-    _check("eagle_tree_attention_paged", load().eagle_tree_attention_paged(
-        ctypes.byref(shape), ctypes.byref(pages), _ptr(q), _ptr(k_pages), _ptr(v_pages),
-        _ptr(page_table), _ptr(prefix_lens), int(shared_len), _ptr(k_tree), _ptr(v_tree),
-        _ptr(parents), _ptr(out), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+    _check("eagle_tree_attention_paged", (_module or _native()).tree_attention_paged(
+        shape, pages, q, k_pages, v_pages, page_table, prefix_lens, shared_len, k_tree, v_tree, parents, out,
+        workspace, stream))
 
 
 def commit_accepted_paged(shape: Shape, pages: Pages, k_pages, v_pages, page_table, prefix_lens,
                           k_tree, v_tree, hidden, parents, accepted_nodes, accept_len,
                           new_prefix_lens, feat, stream=None) -> None:
-    _check("eagle_commit_accepted_paged", load().eagle_commit_accepted_paged(
-        ctypes.byref(shape), ctypes.byref(pages), _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
-        _ptr(prefix_lens), _ptr(k_tree), _ptr(v_tree), _ptr(hidden), _ptr(parents),
-        _ptr(accepted_nodes), _ptr(accept_len), _ptr(new_prefix_lens), _ptr(feat), _stream(stream)))
+    _check("eagle_commit_accepted_paged", (_module or _native()).commit_accepted_paged(
+        shape, pages, k_pages, v_pages, page_table, prefix_lens, k_tree, v_tree, hidden, parents, accepted_nodes,
+        accept_len, new_prefix_lens, feat, stream))
 
 
 # ---------------------------------------------------------------- e4m3 LM head
 
-_DTYPES = {}
-
-
-def _dtype_of(t) -> int:
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16})
-    return _DTYPES[t.dtype]
-
-
 def quantize_rows(x, x_out, scales, stream=None) -> None:
     """x [R, H] fp32 or bf16 -> x_out [R, H] e4m3, scales [ceil(H / 128), R rounded up to 4]."""
-    R, H = x.shape
-    if tuple(x_out.shape) != (R, H) or tuple(scales.shape) != ((H + 127) // 128, (R + 3) // 4 * 4):
-        raise ValueError("x_out is [R, H] and scales [ceil(H / 128), R rounded up to 4]")
-    _check("eagle_quantize_rows", load().eagle_quantize_rows(
-        R, H, _dtype_of(x), _ptr(x), _ptr(x_out), _ptr(scales), _stream(stream)))
+    _check("eagle_quantize_rows", (_module or _native()).quantize_rows(x, x_out, scales, stream))
 
 
 def quantize_blocks(w, w_out, scales, stream=None) -> None:
     """w [V, H] fp32 or bf16 -> w_out [V, H] e4m3, scales [ceil(V / 128), ceil(H / 128)]."""
-    V, H = w.shape
-    if tuple(w_out.shape) != (V, H) or tuple(scales.shape) != ((V + 127) // 128, (H + 127) // 128):
-        raise ValueError("w_out is [V, H] and scales [ceil(V / 128), ceil(H / 128)]")
-    _check("eagle_quantize_blocks", load().eagle_quantize_blocks(
-        V, H, _dtype_of(w), _ptr(w), _ptr(w_out), _ptr(scales), _stream(stream)))
+    _check("eagle_quantize_blocks", (_module or _native()).quantize_blocks(w, w_out, scales, stream))
 
 
 def lm_head_logits_scaled(x, x_scales, w, w_scales, logits, stream=None) -> None:
-    R, H = x.shape
-    V = w.shape[0]
-    KB = (H + 127) // 128
-    if (w.shape[1] != H or tuple(x_scales.shape) != (KB, (R + 3) // 4 * 4) or
-            tuple(w_scales.shape) != ((V + 127) // 128, KB) or tuple(logits.shape) != (R, V)):
-        raise ValueError("operands are x [R, H], x_scales [KB, R rounded up to 4], w [V, H], "
-                         "w_scales [ceil(V / 128), KB] and logits [R, V]")
-    _check("eagle_lm_head_logits_scaled", load().eagle_lm_head_logits_scaled(
-        R, H, V, _ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(logits), _stream(stream)))
+    """x [R, H] and w [V, H] e4m3, x_scales [ceil(H / 128), R rounded up to 4], w_scales [ceil(V / 128),
+    ceil(H / 128)], logits [R, V] fp32."""
+    _check("eagle_lm_head_logits_scaled", (_module or _native()).lm_head_logits_scaled(
+        x, x_scales, w, w_scales, logits, stream))
 
 
 def device_error(reset: bool = True) -> int:

@@ -8,8 +8,10 @@
 // chain); the blocks are scaled and summed in fp32 registers.
 //
 // Two forms, by the number of tree rows (each measured at both sizes, see the kernels):
-//   up to 64 rows    swap-AB like lm_head.cuh: 128 vocabulary rows are the MMA's M, the tree
-//                    rows its N; the weight streams once and bounds it;
+//   up to 32 rows    swap-AB like lm_head.cuh: 128 vocabulary rows are the MMA's M, the tree
+//                    rows its N; the weight streams once and bounds it (a row of
+//                    32000 x 4096: 22 us, 6.0 TB/s; 60 rows of 32000 x 8192: 65 us, the
+//                    other form 53);
 //   more             tree rows as M (128 a tile), one or two blocks of 128 vocabulary rows
 //                    as N, so that a thread's accumulators all share one scale.
 // In both, per K block one 128-deep MMA chain goes into a fresh TMEM buffer and eight
@@ -168,7 +170,7 @@ __host__ __device__ inline size_t scaled_smem_bytes(int bn, int stages) {
   return 1024 + static_cast<size_t>(stages) * scaled_stage_bytes(bn) + (2 * stages + 9) * 8 + 16;
 }
 
-// CW: accumulator columns (tree rows) of an epilogue thread: 8, 16 or 32.
+// CW: accumulator columns (tree rows) of an epilogue thread: 8 or 16.
 template <int CW>
 struct ScaledCfg {
   // TMEM columns of a buffer (tcgen05.alloc takes powers of two from 32), and buffers: two
@@ -177,7 +179,6 @@ struct ScaledCfg {
   static constexpr int kBufs = 4;
 };
 
-__device__ __forceinline__ void tmem_ld_step(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_32x32b_x32(taddr, r); }
 __device__ __forceinline__ void tmem_ld_step(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_32x32b_x16(taddr, r); }
 __device__ __forceinline__ void tmem_ld_step(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"

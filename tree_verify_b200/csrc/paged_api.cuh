@@ -3,6 +3,8 @@
 // eagle_verify.cu, whose helpers it uses.
 #pragma once
 
+#include <atomic>
+
 #include "lm_head_scaled.cuh"
 #include "paged.cuh"
 #include "paged_attention.cuh"
@@ -48,12 +50,20 @@ int elem_size(const eagle_shape_t* s) { return s->dtype == EAGLE_DTYPE_BF16 ? 2 
 
 // ------------------------------------------------------------------ kernel attributes
 
-// Idempotent and cheap: set per call, so that every device gets it.
-template <typename K>
-bool allow_smem(K kernel, int bytes) {
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess) return true;
-  cudaGetLastError();
-  return false;
+// Set once for each device.
+template <auto kKernel>
+bool allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};  // bit per device (kMaxDevices of them)
+  static_assert(kMaxDevices <= 64, "a bit per device");
+  int dev;
+  if (!current_device(&dev)) return false;
+  if ((done.load(std::memory_order_relaxed) >> dev) & 1) return true;
+  if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return true;
 }
 
 // Kernels whose first warps take `inc` registers a thread out of what the CTA was launched
@@ -141,7 +151,7 @@ eagle_status_t launch_paged_f32(const PagedF32Plan& plan, const void* q, const v
                                 const void* kt, const void* vt, void* out, void* ws, const PagedAttnParams& ap,
                                 cudaStream_t st) {
   constexpr int bytes = PagedF32Cfg<D, RT>::kBytes;
-  if (!allow_smem(paged_attn_f32_kernel<D, RT>, bytes)) return EAGLE_ERR_CUDA;
+  if (!allow_smem<paged_attn_f32_kernel<D, RT>>(bytes)) return EAGLE_ERR_CUDA;
   PagedF32Params p{};
   p.a = ap;
   p.q = static_cast<const float*>(q);
@@ -208,7 +218,7 @@ eagle_status_t launch_paged_tc(const eagle_shape_t* s, const eagle_pages_t* pg, 
                                const void* q, const void* kp, const void* vp, const void* kt, const void* vt,
                                void* out, void* ws, cudaStream_t st) {
   static const bool shares = register_shares_fit(paged_attn_tc_kernel<D>, kPgThreads, kPgSoftRegs, kPgOtherRegs);
-  if (!shares || !allow_smem(paged_attn_tc_kernel<D>, PgSmem<D>::kAlloc)) return EAGLE_ERR_CUDA;
+  if (!shares || !allow_smem<paged_attn_tc_kernel<D>>(PgSmem<D>::kAlloc)) return EAGLE_ERR_CUDA;
   const PagedPlan plan = plan_paged(s, ap.shared);
   PagedTcParams p{};
   p.a = ap;
@@ -285,10 +295,10 @@ bool encode_bytes(CUtensorMap* map, const void* base, uint64_t cols, uint64_t ro
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename K>
-eagle_status_t launch_scaled(K kernel, const CUtensorMap& tw, const CUtensorMap& th, const ScaledParams& prm,
+template <auto kKernel>
+eagle_status_t launch_scaled(const CUtensorMap& tw, const CUtensorMap& th, const ScaledParams& prm,
                              unsigned grid, unsigned threads, size_t smem, cudaStream_t st) {
-  if (!allow_smem(kernel, 227 * 1024)) return EAGLE_ERR_CUDA;
+  if (!allow_smem<kKernel>(227 * 1024)) return EAGLE_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
@@ -301,7 +311,7 @@ eagle_status_t launch_scaled(K kernel, const CUtensorMap& tw, const CUtensorMap&
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, tw, th, prm) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kKernel, tw, th, prm) != cudaSuccess) {
     cudaGetLastError();
     return EAGLE_ERR_CUDA;
   }
@@ -524,9 +534,8 @@ eagle_status_t eagle_lm_head_logits_scaled(int32_t rows, int32_t hidden, int32_t
     prm.stages = stages;
     const size_t smem = scaled_smem_bytes(bn, stages);
     const unsigned grid = static_cast<unsigned>(vtiles);
-    if (bn <= 16) return launch_scaled(lm_head_scaled_kernel<8>, tw, th, prm, grid, kScThreads, smem, st);
-    if (bn <= 32) return launch_scaled(lm_head_scaled_kernel<16>, tw, th, prm, grid, kScThreads, smem, st);
-    return launch_scaled(lm_head_scaled_kernel<32>, tw, th, prm, grid, kScThreads, smem, st);
+    if (bn <= 16) return launch_scaled<lm_head_scaled_kernel<8>>(tw, th, prm, grid, kScThreads, smem, st);
+    return launch_scaled<lm_head_scaled_kernel<16>>(tw, th, prm, grid, kScThreads, smem, st);
   }
   // two vocabulary blocks a tile (two thirds of the shared-memory bytes per product) while
   // there are six of them per SM, so that the last round of tiles is a small part
@@ -542,10 +551,10 @@ eagle_status_t eagle_lm_head_logits_scaled(int32_t rows, int32_t hidden, int32_t
     static const bool shares =
         register_shares_fit(lm_head_scaled_rows_kernel<2>, kScRowsThreads, kScRowsEpiRegs, kScRowsOtherRegs);
     if (!shares) return EAGLE_ERR_CUDA;
-    return launch_scaled(lm_head_scaled_rows_kernel<2>, tw, th, prm, grid, kScRowsThreads, ScaledRowsCfg<2>::kAlloc,
+    return launch_scaled<lm_head_scaled_rows_kernel<2>>(tw, th, prm, grid, kScRowsThreads, ScaledRowsCfg<2>::kAlloc,
                          st);
   }
-  return launch_scaled(lm_head_scaled_rows_kernel<1>, tw, th, prm, grid, kScRowsThreads, ScaledRowsCfg<1>::kAlloc, st);
+  return launch_scaled<lm_head_scaled_rows_kernel<1>>(tw, th, prm, grid, kScRowsThreads, ScaledRowsCfg<1>::kAlloc, st);
 }
 
 }  // extern "C"
