@@ -186,9 +186,9 @@ struct PgSmem {
   static constexpr int kFirstOff = kScanOff + 16 * 8 + 16 * 4;  // warp sums and minima
   static constexpr int kBarOff = kFirstOff + 16;
   // q_full[2], k_full, k_empty, v_full, v_empty, s_full[2], p_half[2], p_full[2], pv_done[2],
-  // all_done[2],
+  // turn[2], all_done[2],
   // item_full, item_empty
-  static constexpr int kNumBars = 2 + 2 * kKStages + 2 * kVStages + 10 + 2 * kPgItems;
+  static constexpr int kNumBars = 2 + 2 * kKStages + 2 * kVStages + 12 + 2 * kPgItems;
   static constexpr int kBytes = kBarOff + kNumBars * 8 + 16;
   static constexpr int kAlloc = kBytes + 1024;
   static constexpr uint32_t kTmemCols = 512;
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   const uint32_t k_full = q_full + 16, k_empty = k_full + 8 * SK;
   const uint32_t v_full = k_empty + 8 * SK, v_empty = v_full + 8 * SV;
   const uint32_t s_full = v_empty + 8 * SV, p_half = s_full + 16, p_full = p_half + 16;
-  const uint32_t pv_done = p_full + 16, all_done = pv_done + 16;
+  const uint32_t pv_done = p_full + 16, turn = pv_done + 16, all_done = turn + 16;
   const uint32_t item_full = all_done + 16, item_empty = item_full + 8 * kPgItems;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kBarOff + SM::kNumBars * 8);
 
@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       mbar_init(p_half + 8 * g, 4);  // one arrival per warp of the group
       mbar_init(p_full + 8 * g, 4);
       mbar_init(pv_done + 8 * g, 1);
+      mbar_init(turn + 8 * g, 1);
       mbar_init(all_done + 8 * g, 1);
     }
     for (int s = 0; s < SK; ++s) {
@@ -489,6 +490,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       int base = 0;               // the next one's first tile in the CTA's run of tiles
       int gi = 0, end = 0, step = 1;  // the tiles this group takes of the item
       int n = 0, q = 0;           // tiles done, Q tiles sent for
+      int turns = 0;              // shared tiles done
       prefetch_tmap(&tm_q);
       auto wait = [&](uint32_t bar, uint32_t parity) { ok = ok && mbar_wait(bar, parity, kErrAttnMmaWait); };
       // the next item with a tile for this group, its Q tile on the way
@@ -546,6 +548,11 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         }
         tc_commit(sf);
         tc_commit(k_empty + 8 * sk);
+        // With shared tiles the groups take turns from P V to the next S: left alone they fall
+        // into step, both softmaxes at once and then both pairs of MMAs.
+        const bool alternate = step == 1;
+        if (!first && alternate) mbar_arrive(turn + 8 * (g ^ 1));
+        if (alternate && (g == 1 || turns > 0)) wait(turn + 8 * g, (turns - 1 + g) & 1);
         wait(v_full + 8 * sv, (gi / SV) & 1);
         seen = gi + 1;
         const uint64_t vd = smem_desc_mn_sw128(sbase + SM::kVOff + sv * SM::kTile, kAttnKeys * 128, 1024);
@@ -564,8 +571,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         tc_commit(pd);
         tc_commit(v_empty + 8 * sv);
         first = false;
+        turns += alternate ? 1 : 0;
         gi += step;
         if (gi >= end) {
+          if (alternate) mbar_arrive(turn + 8 * (g ^ 1));
           // (P was taken from a complete S: the Q tile of the item that ends here is free)
           first = true;
           more = open();
