@@ -12,8 +12,8 @@
 // tree.  Keys go in tiles of 128.
 //
 // The lengths live on the device, so the plan is made there: items are laid end to end on
-// a line of units (a key tile costs one unit per row tile, an item kPgItemCost more) and
-// the line is cut into one equal piece for each of P CTAs, one CTA per SM.  Every CTA finds
+// a line of units (paged_tile_units for a key tile, kPgItemCost more for an item) and the
+// line is cut into one equal piece for each of P CTAs, one CTA per SM.  Every CTA finds
 // its piece by a scan over the batch's lengths.  A piece that begins or ends inside an item
 // leaves a partial result; a second kernel merges each row's partials.
 //
@@ -21,7 +21,7 @@
 // scores S and accumulator O in TMEM and its own chain S = Q K^T, softmax, O += P V; one
 // group's softmax runs under the other's MMAs.  With two row tiles in the item the groups
 // take one each and share every K/V tile; with one, they take the even and the odd tiles of
-// the CTA's run and leave a partial each.
+// the CTA's run and add up their sums at its end.
 //
 //   warps 0-3, 4-7   softmax groups 0 and 1
 //   warp 8           TMA of the K and V tiles: one box per page and 64 columns, a lane each
@@ -40,7 +40,7 @@ constexpr int kPgThreads = 32 * 12;
 constexpr int kPgLoadWarp = 8, kPgMmaWarp = 9, kPgItemWarp = 11;
 constexpr int kPgReaders = 11;                // readers of an item: 8 softmax warps, the loads, 2 MMA issuers
 constexpr int kPgItems = 2;                   // items described ahead
-constexpr int kPgItemCost = 4;                // units of an item beyond its tiles
+constexpr int kPgItemCost = 8;                // units of an item beyond its tiles (see paged_tile_units)
 constexpr float kPgRescaleThreshold = 8.0f;   // log2 units
 constexpr int kPgSoftRegs = 208, kPgOtherRegs = 88;  // of the launch's 168 x 384 registers
 constexpr int kPgPolyPairs = 2;               // of 8 pairs, through the polynomial 2^x
@@ -77,21 +77,28 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedTcParams& p, int b) {
   return s;
 }
 
+// Units of a key tile for `nrow` row tiles: a pair costs about 3,750 clocks, bound by its
+// softmax and MMAs; a single row tile half of that, or 2,800 while its K/V come from HBM.
+__device__ __forceinline__ int paged_tile_units(int nrow) { return nrow == 2 ? 4 : 3; }
 // Units of `T` tiles over `rb` row tiles of one kv head.
 __device__ __forceinline__ int64_t paged_head_units(int T, int rb) {
-  return static_cast<int64_t>(rb) * T + ((rb + 1) >> 1) * kPgItemCost;
+  return static_cast<int64_t>(rb >> 1) * (4 * T + kPgItemCost) + (rb & 1) * (3 * T + kPgItemCost);
 }
 // First unit of row pair pi among its head's.
 __device__ __forceinline__ int64_t paged_pair_units(int T, int pi) {
-  return static_cast<int64_t>(pi) * (2 * T + kPgItemCost);
+  return static_cast<int64_t>(pi) * (4 * T + kPgItemCost);
+}
+// Quotient of non-negative numbers, by the short division where it does.
+__device__ __forceinline__ int64_t paged_div(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
 // Pieces of a line of W units: no more than units, so that none is empty.
 __device__ __forceinline__ int paged_pieces(int64_t W, int ctas) { return W < ctas ? static_cast<int>(W) : ctas; }
-// CTA whose piece holds unit u: piece c is [c W / P, (c + 1) W / P).  Lines of fewer than
-// 2^24 units (all but the very largest) take the short division.
+// Piece c is [c W / P, (c + 1) W / P); the CTA whose piece holds unit u.
+__device__ __forceinline__ int64_t paged_cut(int c, int64_t W, int P) { return paged_div(c * W, P); }
 __device__ __forceinline__ int paged_owner(int64_t u, int64_t W, int P) {
-  if (W < (1 << 24)) return static_cast<int>((static_cast<uint32_t>(u + 1) * static_cast<uint32_t>(P) - 1u) / static_cast<uint32_t>(W));
-  return static_cast<int>(((u + 1) * P - 1) / W);
+  return static_cast<int>(paged_div((u + 1) * P - 1, W));
 }
 
 // Walks the items of a piece [lo, hi) of the line.
@@ -126,13 +133,14 @@ struct PagedCursor {
       set_seq(p);
     }
     const int64_t per = paged_head_units(T, rb);
-    kvh = static_cast<int32_t>((lo - base) / per);
-    const int64_t r = (lo - base) % per;
-    pi = static_cast<int32_t>(min(r / (2 * T + kPgItemCost), static_cast<int64_t>(((rb + 1) >> 1) - 1)));
+    kvh = static_cast<int32_t>(paged_div(lo - base, per));
+    const int64_t r = lo - base - kvh * per;
+    pi = static_cast<int32_t>(min(paged_div(r, 4 * static_cast<int64_t>(T) + kPgItemCost),
+                                  static_cast<int64_t>(((rb + 1) >> 1) - 1)));
     u0 = base + kvh * per + paged_pair_units(T, pi);
   }
   __device__ __forceinline__ void next(const PagedTcParams& p) {
-    u0 += static_cast<int64_t>(nrow()) * T + kPgItemCost;
+    u0 += static_cast<int64_t>(paged_tile_units(nrow())) * T + kPgItemCost;
     if (++pi < ((rb + 1) >> 1)) return;
     pi = 0;
     if (++kvh < p.a.Hkv) return;
@@ -142,9 +150,9 @@ struct PagedCursor {
   }
   // the item's tiles [a, z) that start in [lo, hi)
   __device__ __forceinline__ void range(int64_t lo, int64_t hi, int& a, int& z) const {
-    const int w = nrow();
-    a = lo <= u0 ? 0 : static_cast<int>(min((lo - u0 + w - 1) / w, static_cast<int64_t>(T)));
-    z = hi <= u0 ? 0 : static_cast<int>(min((hi - u0 + w - 1) / w, static_cast<int64_t>(T)));
+    const int w = paged_tile_units(nrow());
+    a = lo <= u0 ? 0 : static_cast<int>(min(paged_div(lo - u0 + w - 1, w), static_cast<int64_t>(T)));
+    z = hi <= u0 ? 0 : static_cast<int>(min(paged_div(hi - u0 + w - 1, w), static_cast<int64_t>(T)));
   }
 };
 
@@ -180,10 +188,11 @@ struct PgSmem {
   static constexpr int kQOff = 0;                       // two Q tiles
   static constexpr int kKOff = kQOff + 2 * kTile;
   static constexpr int kVOff = kKOff + kKStages * kTile;
-  static constexpr int kAncOff = kVOff + kVStages * kTile;       // [kPgItems][64] masks
-  static constexpr int kRunOff = kAncOff + kPgItems * 64 * 8;
-  static constexpr int kScanOff = kRunOff + kPgItems * static_cast<int>(sizeof(PagedRun));
-  static constexpr int kFirstOff = kScanOff + 16 * 8 + 16 * 4;  // warp sums and minima
+  static constexpr int kAncOff = kVOff + kVStages * kTile;       // 64 masks
+  static constexpr int kRunOff = kAncOff + 64 * 8;
+  // the groups' exchange, [128] float2; before the first item the plan's warp sums and minima
+  static constexpr int kXchOff = kRunOff + kPgItems * static_cast<int>(sizeof(PagedRun));
+  static constexpr int kFirstOff = kXchOff + 128 * 8;
   static constexpr int kBarOff = kFirstOff + 16;
   // q_full[2], k_full, k_empty, v_full, v_empty, s_full[2], p_half[2], p_full[2], pv_done[2],
   // turn[2], all_done[2],
@@ -194,8 +203,11 @@ struct PgSmem {
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kOCol = 2 * kAttnKeys;      // O of group g at kOCol + g D
   static_assert(kAlloc <= 227 * 1024, "shared memory");
-  static_assert(kScanOff % 8 == 0 && kBarOff % 8 == 0, "alignment");
+  static_assert(kXchOff % 8 == 0 && kBarOff % 8 == 0, "alignment");
 };
+
+// Both softmax groups.
+__device__ __forceinline__ void both_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 template <int D>
 __global__ void __launch_bounds__(kPgThreads, 1)
@@ -210,8 +222,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   uint64_t* anc = reinterpret_cast<uint64_t*>(smem + SM::kAncOff);
   PagedRun* runs = reinterpret_cast<PagedRun*>(smem + SM::kRunOff);
-  int64_t* scan_s = reinterpret_cast<int64_t*>(smem + SM::kScanOff);
+  int64_t* scan_s = reinterpret_cast<int64_t*>(smem + SM::kXchOff);
   int32_t* live_s = reinterpret_cast<int32_t*>(scan_s + 16);
+  float2* xch = reinterpret_cast<float2*>(smem + SM::kXchOff);
   int64_t* first_base_s = reinterpret_cast<int64_t*>(smem + SM::kFirstOff);
   int32_t* first_b_s = reinterpret_cast<int32_t*>(first_base_s + 1);
   const uint32_t q_full = sbase + SM::kBarOff;
@@ -227,7 +240,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   const int cta = blockIdx.x;
 
   // ------------------------------------------------------------ set-up and plan
-  if (tid == 0) {
+  if (tid == 32 * kPgItemWarp) {  // (not a thread that reads lengths in an ordinary batch)
     for (int g = 0; g < 2; ++g) {
       mbar_init(q_full + 8 * g, 1);
       mbar_init(s_full + 8 * g, 1);
@@ -295,7 +308,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       run_shared ? Hkv * paged_head_units((prm.a.shared + kAttnKeys - 1) / kAttnKeys, prm.rb_sh) : 0;
   const int64_t W = shared_units + own_units;
   const int P = paged_pieces(W, prm.ctas);
-  const int64_t lo = cta < P ? cta * W / P : W, hi = cta < P ? (cta + 1) * W / P : W;
+  const int64_t lo = cta < P ? paged_cut(cta, W, P) : W, hi = cta < P ? paged_cut(cta + 1, W, P) : W;
   start += shared_units;
   if (cta == 0 && tid == 0) {
     prm.plan[0] = W;
@@ -304,10 +317,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   {
     const int64_t at = max(lo, shared_units);  // the first own unit this CTA may meet
     int64_t u = start;
-    if (cta == 0 || (at >= start && at < start + sum)) {
+    if (sum > 0 && (cta == 0 || (at >= start && at < start + sum))) {
       for (int b = sb0; b < sb1; ++b) {
-        const PagedSeq s = paged_seq(prm, b);
-        const int64_t units = Hkv * paged_head_units(s.n + 1, prm.rb_own);
+        const int64_t units = chunk == 1 ? sum : Hkv * paged_head_units(paged_seq(prm, b).n + 1, prm.rb_own);
         if (cta == 0) prm.plan[2 + b] = u;
         if (at >= u && at < u + units) {
           *first_b_s = b;
@@ -329,7 +341,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     reg_dec<kPgOtherRegs>();
     if (warp == kPgItemWarp) {
       // ---------------------------------------------------------- items
-      int i = 0;
+      int i = 0, mask_b = -1;  // the masks are of sequence mask_b
       bool ok = true;
       PagedCursor cur;
       if (lo < hi)
@@ -341,7 +353,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         int a = 0, z = 0;
         if (!end) {
           // (a piece that ends in what an item costs beyond its tiles has no run of it)
-          if (lo >= cur.u0 + static_cast<int64_t>(cur.nrow()) * cur.T) {
+          if (lo >= cur.u0 + static_cast<int64_t>(paged_tile_units(cur.nrow())) * cur.T) {
             cur.next(prm);
             continue;
           }
@@ -350,7 +362,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         // the ancestor masks of the tree: a node and every node up its parent chain (a link
         // that does not point to an earlier node ends it); lane j has nodes j and j + 32
         uint64_t m0 = 0, m1 = 0;
-        const bool tree = !end && cur.b >= 0 && z == cur.T;
+        const bool tree = !end && cur.b >= 0 && z == cur.T && cur.b != mask_b;
         if (tree) {
           const int32_t* par = prm.a.parents + static_cast<size_t>(cur.b) * N;
           const int j0 = lane, j1 = lane + 32;
@@ -368,11 +380,14 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         }
         const int s = i % kPgItems;
         if (i >= kPgItems) ok = mbar_wait(item_empty + 8 * s, (i / kPgItems - 1) & 1, kErrAttnProducerWait);
+        // (new masks only once nobody reads the old ones for the item before)
+        if (tree && i > 0) ok = ok && mbar_wait(item_empty + 8 * ((i - 1) % kPgItems), ((i - 1) / kPgItems) & 1, kErrAttnProducerWait);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (tree) {
-          anc[s * 64 + lane] = m0;
-          anc[s * 64 + lane + 32] = m1;
+          anc[lane] = m0;
+          anc[lane + 32] = m1;
+          mask_b = cur.b;
         }
         if (lane == 0) {
           PagedRun& d = runs[s];
@@ -611,9 +626,11 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       const PagedRun& d = runs[i % kPgItems];
       const int b = d.b, nrow = d.nrow, a = d.a, z = d.z, tree_t = d.n, L = d.L, begin = d.begin, t0 = d.t0;
       const int node = d.node0 + (nrow == 2 ? g * prm.NB : 0) + row_node;  // in the batch or in the sequence
-      const int64_t prow = d.prow + g * (b < 0 ? prm.rows_sh : prm.rows_own);
+      const int rows = b < 0 ? prm.rows_sh : prm.rows_own;
+      const int64_t prow = d.prow + (nrow == 2 ? g * rows : 0);
+      const int kvh = d.kvh;
       const bool in_tile = r < prm.NB * G;
-      const uint64_t tree_bits = in_tile && b >= 0 && node < N ? anc[(i % kPgItems) * 64 + node] : 0ull;
+      const uint64_t tree_bits = in_tile && b >= 0 && node < N ? anc[node] : 0ull;
       __syncwarp();
       if (lane == 0) run_release(i);
       if (b == kPgEnd) break;
@@ -755,31 +772,89 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full + 8 * g);
       }
-      // ---------------------------------------------------------- the run's partial
-      // [D / 4][rows of the tile][4]: a warp's stores are contiguous
-      if (t_first < z) {
+      // ---------------------------------------------------------- the run's result
+      // A run of all of an item's tiles, without a shared part beside it, is the output;
+      // others leave a partial, [D / 4][rows of the tile][4]: a warp's stores are contiguous.
+      const bool direct = b >= 0 && a == 0 && z == tree_t + 1 && !(run_shared && L >= prm.a.shared);
+      __nv_bfloat16* orow =
+          prm.out + ((static_cast<int64_t>(max(b, 0)) * N + node) * prm.a.Hq + kvh * G + r % G) * D;
+      float4* part = reinterpret_cast<float4*>(prm.part_acc + prow * D) + r;
+      auto put = [&](int cc, const float (&v)[16]) {
+        if (!rvalid) return;
+        if (direct) {
+#pragma unroll
+          for (int k = 0; k < 16; k += 8)
+            *reinterpret_cast<uint4*>(orow + cc + k) =
+                make_uint4(pack_bf16x2(v[k], v[k + 1]), pack_bf16x2(v[k + 2], v[k + 3]),
+                           pack_bf16x2(v[k + 4], v[k + 5]), pack_bf16x2(v[k + 6], v[k + 7]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; k += 4)
+            part[static_cast<size_t>((cc + k) / 4) * rows] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+        }
+      };
+      const bool any = nrow == 2 ? z > a : z > t_first;  // this group took a tile
+      if (any) {
         wait(pv_done + 8 * g, (n - 1) & 1);
         tc_fence_after();
-        if (live) {
-          const int rows = b < 0 ? prm.rows_sh : prm.rows_own;
-          float4* dst = reinterpret_cast<float4*>(prm.part_acc + prow * D) + r;
-#pragma unroll 1
-          for (int cc = 0; cc < D; cc += 32) {
-            uint32_t o[32];
-            __syncwarp();
-            tmem_ld_cols<32>(o_col + cc, o);
-            tmem_ld_wait();
-            if (rvalid) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                dst[static_cast<size_t>(cc / 4 + k) * rows] =
-                    make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
-            }
+      }
+      // what this row's O, and the other group's where the groups took alternate tiles of the
+      // same rows, count for
+      float w0 = direct ? 1.0f / l : 1.0f, w1 = 0.f;
+      int c0 = 0, c1 = D;
+      if (nrow == 1) {
+        // the sums meet here: both O are in this warp's TMEM lanes, and each group brings half
+        // of the columns out
+        if (g == 1) xch[r] = make_float2(m_ref, l);
+        tc_fence_before();
+        both_sync();
+        if (g == 0) {
+          const float2 x = xch[r];
+          const float m = fmaxf(m_ref, x.x);
+          w0 = m_ref == -INFINITY ? 0.f : exp2f(m_ref - m);
+          w1 = x.x == -INFINITY ? 0.f : exp2f(x.x - m);
+          m_ref = m;
+          l = l * w0 + x.y * w1;
+          if (direct) {
+            w0 /= l;
+            w1 /= l;
           }
+          xch[r] = make_float2(w1, w0);
+        }
+        both_sync();
+        tc_fence_after();
+        if (g == 1) {
+          w0 = xch[r].x;
+          w1 = xch[r].y;
+        }
+        c0 = g * (D / 2);
+        c1 = c0 + D / 2;
+      }
+      if (live && z > a) {
+        const uint32_t other = lane_base + SM::kOCol + (g ^ 1) * D;
+#pragma unroll 1
+        for (int cc = c0; cc < c1; cc += 16) {
+          uint32_t o[16];
+          float v[16];
+          __syncwarp();
+          tmem_ld_cols<16>(o_col + cc, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = w0 > 0.f ? __uint_as_float(o[k]) * w0 : 0.f;
+          if (nrow == 1) {
+            tmem_ld_cols<16>(other + cc, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] += w1 > 0.f ? __uint_as_float(o[k]) * w1 : 0.f;
+          }
+          put(cc, v);
         }
       }
-      if (rvalid) prm.part_ml[prow + r] = make_float2(m_ref, l);
+      if (rvalid && !direct && (nrow == 2 || g == 0)) prm.part_ml[prow + r] = make_float2(m_ref, l);
+      if (nrow == 1) {  // neither group lets its next P V at its O before the other has read it
+        tc_fence_before();
+        both_sync();
+      }
       base += z - a;
     }
   }
@@ -825,22 +900,23 @@ __global__ void __launch_bounds__(kSplit ? 256 : 2 * D) paged_attn_merge_kernel(
       const int node = in_head / G, hg = in_head - node * G;
       const uint32_t fnode = b * N + node;
       orow = static_cast<int64_t>(fnode) * Hq + kvh * G + hg;
+      // (all of these are on their way before the first is used)
+      const int64_t W = prm.plan[0], shared_runs = prm.plan[1], own_start = prm.plan[2 + b];
       const PagedSeq s = paged_seq(prm, b);
-      if (k == 0 || (prm.plan[1] != 0 && s.L >= prm.a.shared)) {
-        const int64_t W = prm.plan[0];
+      if (k == 0 || (shared_runs != 0 && s.L >= prm.a.shared)) {
         const int P = paged_pieces(W, prm.ctas);
         const uint32_t nd = k == 0 ? node : fnode;
         const int rb = k == 0 ? prm.rb_own : prm.rb_sh;
         const int rt = nd / static_cast<uint32_t>(prm.NB), pi = rt >> 1;
         const int nrow = min(2, rb - 2 * pi);
         const int T = k == 0 ? s.n + 1 : (prm.a.shared + kAttnKeys - 1) / kAttnKeys;
-        const int64_t u0 = (k == 0 ? prm.plan[2 + b] : 0) + kvh * paged_head_units(T, rb) + paged_pair_units(T, pi);
+        const int64_t u0 = (k == 0 ? own_start : 0) + kvh * paged_head_units(T, rb) + paged_pair_units(T, pi);
         const int c0 = paged_owner(u0, W, P);
-        const int c1 = paged_owner(u0 + static_cast<int64_t>(T - 1) * nrow, W, P);
-        // a pair's row tile is one group's; a single row tile has a partial of either group
+        const int c1 = paged_owner(u0 + static_cast<int64_t>(T - 1) * paged_tile_units(nrow), W, P);
+        // (of a pair, the second row tile has the second slot)
         row0 = paged_part_row(prm, k == 0 ? b : -1, kvh, pi, c0, nrow == 2 ? (rt & 1) : 0);
-        step = (nrow == 2 ? 2 : 1) * (k == 0 ? prm.rows_own : prm.rows_sh);
-        count = (c1 - c0 + 1) * (nrow == 2 ? 1 : 2);
+        step = 2 * (k == 0 ? prm.rows_own : prm.rows_sh);
+        count = c1 - c0 + 1;
         // the row in the tile, below the bits of the partial's first row
         row0 = row0 * 128 + ((nd - rt * prm.NB) * G + hg);
       }
@@ -856,6 +932,7 @@ __global__ void __launch_bounds__(kSplit ? 256 : 2 * D) paged_attn_merge_kernel(
 #pragma unroll 1
   for (int j = lane & 7; j < kRows; j += 8) {
     const int n0 = count_s[0][j], total = n0 + count_s[1][j];
+    if (!kSplit && total <= 1) continue;  // the run that holds the whole item wrote the output (0: no row)
     const int64_t base0 = row0_s[0][j] >> 7, base1 = row0_s[1][j] >> 7;
     const int r0 = static_cast<int>(row0_s[0][j] & 127), r1 = static_cast<int>(row0_s[1][j] & 127);
     const int st0 = step_s[0][j], st1 = step_s[1][j];
@@ -914,7 +991,7 @@ __global__ void __launch_bounds__(kSplit ? 256 : 2 * D) paged_attn_merge_kernel(
         acc = make_float4(acc.x + w * t.x, acc.y + w * t.y, acc.z + w * t.z, acc.w + w * t.w);
       }
     }
-    if (out_s[j] < 0) continue;
+    if (total <= 1) continue;
     const float inv = 1.0f / den;  // the node itself is always visible
     *reinterpret_cast<uint2*>(prm.out + out_s[j] * D + col * 4) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
