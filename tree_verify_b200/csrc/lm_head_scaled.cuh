@@ -8,10 +8,9 @@
 // chain); the blocks are scaled and summed in fp32 registers.
 //
 // Two forms, by the number of tree rows (each measured at both sizes, see the kernels):
-//   up to 32 rows    swap-AB like lm_head.cuh: 128 vocabulary rows are the MMA's M, the tree
+//   up to 16 rows    swap-AB like lm_head.cuh: 128 vocabulary rows are the MMA's M, the tree
 //                    rows its N; the weight streams once and bounds it (a row of
-//                    32000 x 4096: 22 us, 6.0 TB/s; 60 rows of 32000 x 8192: 65 us, the
-//                    other form 53);
+//                    32000 x 4096: 22 us, 6.0 TB/s, the other form 32; 32 rows: 27 and 25);
 //   more             tree rows as M (128 a tile), one or two blocks of 128 vocabulary rows
 //                    as N, so that a thread's accumulators all share one scale.
 // In both, per K block one 128-deep MMA chain goes into a fresh TMEM buffer and eight
@@ -27,7 +26,7 @@ namespace eagle {
 constexpr int kScBlock = 128;        // elements that share a scale; vocabulary rows per CTA
 constexpr int kScThreads = 32 * 10;  // TMA, MMA, 8 epilogue warps
 constexpr int kScEpiWarps = 8;
-constexpr int kScFewRows = 32;       // rows up to which the weight is the MMA's M
+constexpr int kScFewRows = 16;       // rows up to which the weight is the MMA's M
 
 // 2^e and 2^-e for the smallest e >= -126 with amax <= 448 * 2^e: amax = m * 2^k with
 // 1 <= m < 2, and 448 = 1.75 * 2^8, so e = k - 8 while m <= 1.75 and k - 7 above.  The
@@ -170,27 +169,19 @@ __host__ __device__ inline size_t scaled_smem_bytes(int bn, int stages) {
   return 1024 + static_cast<size_t>(stages) * scaled_stage_bytes(bn) + (2 * stages + 9) * 8 + 16;
 }
 
-// CW: accumulator columns (tree rows) of an epilogue thread: 8 or 16.
-template <int CW>
-struct ScaledCfg {
-  // TMEM columns of a buffer (tcgen05.alloc takes powers of two from 32), and buffers: two
-  // CTAs of an SM fit their 512 columns together
-  static constexpr int kCols = 2 * CW < 32 ? 32 : 2 * CW;
-  static constexpr int kBufs = 4;
-};
+constexpr int kScCW = 8;      // accumulator columns (tree rows) of an epilogue thread
+constexpr int kScCols = 32;   // TMEM columns of a buffer (the least that can be allocated)
+constexpr int kScBufs = 4;    // two CTAs of an SM fit TMEM's 512 columns together
 
-__device__ __forceinline__ void tmem_ld_step(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_32x32b_x16(taddr, r); }
-__device__ __forceinline__ void tmem_ld_step(uint32_t taddr, uint32_t (&r)[8]) {
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
 
-template <int CW>
 __global__ void __launch_bounds__(kScThreads, 2)
     lm_head_scaled_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_h,
                           const ScaledParams prm) {
-  using C = ScaledCfg<CW>;
   extern __shared__ uint8_t sc_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sc_smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -215,7 +206,7 @@ __global__ void __launch_bounds__(kScThreads, 2)
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
-    for (int u = 0; u < C::kBufs; ++u) {
+    for (int u = 0; u < kScBufs; ++u) {
       mbar_init(smem_u32(&acc_full[u]), 1);
       mbar_init(smem_u32(&acc_empty[u]), kScEpiWarps);
     }
@@ -223,7 +214,7 @@ __global__ void __launch_bounds__(kScThreads, 2)
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), C::kCols * C::kBufs);
+    tmem_alloc(smem_u32(tmem_slot), kScCols * kScBufs);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -257,9 +248,9 @@ __global__ void __launch_bounds__(kScThreads, 2)
       // ---------------- MMA issuer
       const uint32_t idesc = idesc_e4m3_f32(kScBlock, bn);
       for (int kb = 0; kb < KB; ++kb) {
-        const int s = kb % S, u = kb % C::kBufs;
-        bool ok = kb < C::kBufs ||
-                  mbar_wait(smem_u32(&acc_empty[u]), (kb / C::kBufs - 1) & 1, kErrLmMmaWait);
+        const int s = kb % S, u = kb % kScBufs;
+        bool ok = kb < kScBufs ||
+                  mbar_wait(smem_u32(&acc_empty[u]), (kb / kScBufs - 1) & 1, kErrLmMmaWait);
         ok = ok && mbar_wait(smem_u32(&full[s]), (kb / S) & 1, kErrLmMmaWait);
         if (!ok) break;
         tc_fence_after();
@@ -267,7 +258,7 @@ __global__ void __launch_bounds__(kScThreads, 2)
         const uint64_t b = smem_desc_k_sw128(smem_u32(h_tiles + s * bn * kScBlock));
 #pragma unroll
         for (int k = 0; k < kScBlock / 32; ++k)
-          tc_mma_f8(tmem + static_cast<uint32_t>(u * C::kCols), a + 2 * k, b + 2 * k, idesc, k > 0 ? 1u : 0u);
+          tc_mma_f8(tmem + static_cast<uint32_t>(u * kScCols), a + 2 * k, b + 2 * k, idesc, k > 0 ? 1u : 0u);
         tc_commit(smem_u32(&empty[s]));
         tc_commit(smem_u32(&acc_full[u]));
       }
@@ -280,31 +271,31 @@ __global__ void __launch_bounds__(kScThreads, 2)
     // ---------------- epilogue: TMEM -> scaled sums in registers -> global
     const int quarter = warp & 3;         // TMEM lanes this warp may access
     const int grp = (warp - 2) >> 2;      // half of the tree rows
-    const int col0 = grp * CW;
+    const int col0 = grp * kScCW;
     const int v = v0 + quarter * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(col0);
     const float* wsv = prm.ws + static_cast<size_t>(vb) * KB;
-    // the row scales come through L1 (every lane reads the same ones); columns past the
-    // last row take the scales of rows that exist, for sums that are not stored
+    // the row scales come through L1 (every lane reads the same ones); columns past the last
+    // row take the scales of rows that exist, for sums that are not stored
     const int last4 = prm.ldm / 4 - 1;
     const bool any = col0 < prm.M;
-    float2 acc[CW / 2];
+    float2 acc[kScCW / 2];
 #pragma unroll
-    for (int j = 0; j < CW / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+    for (int j = 0; j < kScCW / 2; ++j) acc[j] = make_float2(0.f, 0.f);
     float w_next = wsv[0];
     bool ok = true;
     for (int kb = 0; kb < KB; ++kb) {
-      const int u = kb % C::kBufs;
+      const int u = kb % kScBufs;
       const float w = w_next;
       if (kb + 1 < KB) w_next = wsv[kb + 1];
       const float4* hs = reinterpret_cast<const float4*>(prm.hs + static_cast<size_t>(kb) * prm.ldm);
-      ok = ok && mbar_wait(smem_u32(&acc_full[u]), (kb / C::kBufs) & 1, kErrLmEpilogueWait);
+      ok = ok && mbar_wait(smem_u32(&acc_full[u]), (kb / kScBufs) & 1, kErrLmEpilogueWait);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      uint32_t d[CW];
+      uint32_t d[kScCW];
       if (any) {
-        tmem_ld_step(lane_base + static_cast<uint32_t>(u * C::kCols), d);
+        tmem_ld_32x32b_x8(lane_base + static_cast<uint32_t>(u * kScCols), d);
         tmem_ld_wait();
       }
       tc_fence_before();
@@ -312,7 +303,7 @@ __global__ void __launch_bounds__(kScThreads, 2)
       if (lane == 0) mbar_arrive(smem_u32(&acc_empty[u]));
       if (any) {
 #pragma unroll
-        for (int j = 0; j < CW / 4; ++j) {
+        for (int j = 0; j < kScCW / 4; ++j) {
           const float4 h4 = __ldg(hs + min(col0 / 4 + j, last4));
           const float2 s0 = fmul2(make_float2(h4.x, h4.y), make_float2(w, w));
           const float2 s1 = fmul2(make_float2(h4.z, h4.w), make_float2(w, w));
@@ -324,7 +315,7 @@ __global__ void __launch_bounds__(kScThreads, 2)
     }
     if (ok && v < prm.V) {
 #pragma unroll
-      for (int j = 0; j < CW; ++j) {
+      for (int j = 0; j < kScCW; ++j) {
         if (col0 + j < prm.M)
           prm.logits[static_cast<size_t>(col0 + j) * prm.V + v] = (j & 1) ? acc[j / 2].y : acc[j / 2].x;
       }
@@ -334,7 +325,7 @@ __global__ void __launch_bounds__(kScThreads, 2)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kCols * C::kBufs);
+    tmem_dealloc(tmem, kScCols * kScBufs);
   }
 }
 
@@ -357,13 +348,20 @@ constexpr int kScRowsThreads = 32 * 12;
 constexpr int kScRowsTmaWarp = 8, kScRowsMmaWarp = 9;
 constexpr int kScRowsEpiRegs = 208, kScRowsOtherRegs = 88;  // of the launch's 168 x 384 registers
 
-template <int NV>
+// NV: vocabulary blocks of a tile; kRows: rows of hidden that are loaded, 128 or 64 (the MMA
+// then reads the weight's bytes as rows 64-127, whose sums nobody takes).
+template <int NV, int kRows>
 struct ScaledRowsCfg {
   static constexpr int kN = kScBlock * NV;          // vocabulary rows of a tile
   static constexpr int kCW = kN / 2;                // accumulators of a thread
-  static constexpr int kStage = kScTile * (1 + NV);
-  static constexpr int kStages = NV == 2 ? 4 : 6;
-  static constexpr int kBufs = 512 / kN;            // all of TMEM
+  // K blocks of a ring slot and of a hand-off: two where TMEM has room for two buffers of two
+  static constexpr int kKB = NV == 2 ? 1 : 2;
+  static constexpr int kHBytes = kRows * kScBlock;
+  static constexpr int kBlock = kHBytes + NV * kScTile;  // one K block's operands
+  static constexpr int kStage = kBlock * kKB;
+  static constexpr int kStages = kRows == 64 ? 4 : (NV == 2 ? 4 : 3);
+  static constexpr int kCols = kN * kKB;            // TMEM columns of a buffer
+  static constexpr int kBufs = 512 / kCols;         // all of TMEM
   static constexpr int kPatch = 32 * 64;            // a warp's 32 rows x 16 columns
   static constexpr int kPatchOff = kStages * kStage;
   static constexpr int kBarOff = kPatchOff + kScEpiWarps * kPatch;
@@ -372,12 +370,12 @@ struct ScaledRowsCfg {
   static_assert(kAlloc <= 227 * 1024, "shared memory");
 };
 
-template <int NV>
+template <int NV, int kRows>
 __global__ void __launch_bounds__(kScRowsThreads, 1)
     lm_head_scaled_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_h,
                                const ScaledParams prm) {
-  using C = ScaledRowsCfg<NV>;
-  constexpr int S = C::kStages, kBufs = C::kBufs, CW = C::kCW;
+  using C = ScaledRowsCfg<NV, kRows>;
+  constexpr int S = C::kStages, kBufs = C::kBufs, CW = C::kCW, KPS = C::kKB;
   extern __shared__ uint8_t scr_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(scr_smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -386,7 +384,7 @@ __global__ void __launch_bounds__(kScRowsThreads, 1)
   const uint32_t acc_empty = acc_full + 8 * kBufs, mma_done = acc_empty + 8 * kBufs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + (2 * S + 2 * kBufs + 1) * 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int KB = prm.KB, row_tiles = prm.bn;
+  const int KB = prm.KB, KS = (KB + KPS - 1) / KPS, row_tiles = prm.bn;
   const int64_t tiles = static_cast<int64_t>(prm.stages) * row_tiles;
 
   if (threadIdx.x == 0) {
@@ -426,17 +424,23 @@ __global__ void __launch_bounds__(kScRowsThreads, 1)
       bool ok = true;
       for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
         const int vt = static_cast<int>(t / row_tiles), rt = static_cast<int>(t % row_tiles);
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int ks = 0; ks < KS; ++ks) {
           if (issued >= S && !mbar_wait(empty + 8 * s, phase, kErrLmProducerWait)) {
             ok = false;
             break;
           }
           const uint32_t fb = full + 8 * s, dst = sbase + s * C::kStage;
           mbar_arrive_expect_tx(fb, C::kStage);
-          tma_load_2d_hint(dst, &tm_h, fb, kb * kScBlock, rt * kScBlock, pol_h);
+          // (a block past the last comes in as zeros)
 #pragma unroll
-          for (int b = 0; b < NV; ++b)
-            tma_load_2d_hint(dst + (1 + b) * kScTile, &tm_w, fb, kb * kScBlock, (vt * NV + b) * kScBlock, pol_w);
+          for (int j = 0; j < KPS; ++j) {
+            const int x = (ks * KPS + j) * kScBlock;
+            const uint32_t at = dst + j * C::kBlock;
+            tma_load_2d_hint(at, &tm_h, fb, x, rt * kScBlock, pol_h);
+#pragma unroll
+            for (int b = 0; b < NV; ++b)
+              tma_load_2d_hint(at + C::kHBytes + b * kScTile, &tm_w, fb, x, (vt * NV + b) * kScBlock, pol_w);
+          }
           ++issued;
           if (++s == S) {
             s = 0;
@@ -456,16 +460,22 @@ __global__ void __launch_bounds__(kScRowsThreads, 1)
       int64_t n = 0;
       bool ok = true;
       for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int ks = 0; ks < KS; ++ks) {
           ok = (n < kBufs || mbar_wait(acc_empty + 8 * u, pu, kErrLmMmaWait)) &&
                mbar_wait(full + 8 * s, ph, kErrLmMmaWait);
           if (!ok) break;
           tc_fence_after();
           const uint64_t a = smem_desc_k_sw128(sbase + s * C::kStage);
-          const uint64_t b = smem_desc_k_sw128(sbase + s * C::kStage + kScTile);
+          const uint64_t b = smem_desc_k_sw128(sbase + s * C::kStage + C::kHBytes);
 #pragma unroll
-          for (int k = 0; k < kScBlock / 32; ++k)
-            tc_mma_f8(tmem + static_cast<uint32_t>(u * C::kN), a + 2 * k, b + 2 * k, idesc, k > 0 ? 1u : 0u);
+          for (int j = 0; j < KPS; ++j) {
+#pragma unroll
+            for (int k = 0; k < kScBlock / 32; ++k) {
+              const uint32_t off = j * (C::kBlock / 16) + 2 * k;
+              tc_mma_f8(tmem + static_cast<uint32_t>(u * C::kCols + j * C::kN), a + off, b + off, idesc,
+                        k > 0 ? 1u : 0u);
+            }
+          }
           tc_commit(empty + 8 * s);
           tc_commit(acc_full + 8 * u);
           ++n;
@@ -505,42 +515,52 @@ __global__ void __launch_bounds__(kScRowsThreads, 1)
       float2 acc[CW / 2];
 #pragma unroll
       for (int j = 0; j < CW / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-      // scales are loaded three blocks ahead (about an L2 round trip)
-      float w1 = __ldg(wsv), h1 = __ldg(hsv), w2 = 0.f, h2 = 0.f, w3 = 0.f, h3 = 0.f;
-      if (KB > 1) {
-        w2 = __ldg(wsv + 1);
-        h2 = __ldg(hsv + prm.ldm);
-      }
-      if (KB > 2) {
-        w3 = __ldg(wsv + 2);
-        h3 = __ldg(hsv + 2 * static_cast<size_t>(prm.ldm));
-      }
-      for (int kb = 0; kb < KB; ++kb) {
-        const float sc = w1 * h1;
-        w1 = w2;
-        h1 = h2;
-        w2 = w3;
-        h2 = h3;
-        if (kb + 3 < KB) {
-          w3 = __ldg(wsv + kb + 3);
-          h3 = __ldg(hsv + static_cast<size_t>(kb + 3) * prm.ldm);
+      // scales are loaded three hand-offs ahead (about an L2 round trip); 0 past the last block
+      float w1[KPS], h1[KPS], w2[KPS], h2[KPS], w3[KPS], h3[KPS];
+      auto scales = [&](int ks, float (&w)[KPS], float (&h)[KPS]) {
+#pragma unroll
+        for (int j = 0; j < KPS; ++j) {
+          const int kb = ks * KPS + j;
+          w[j] = h[j] = 0.f;
+          if (kb < KB) {
+            w[j] = __ldg(wsv + kb);
+            h[j] = __ldg(hsv + static_cast<size_t>(kb) * prm.ldm);
+          }
         }
+      };
+      scales(0, w1, h1);
+      scales(1, w2, h2);
+      scales(2, w3, h3);
+      for (int ks = 0; ks < KS; ++ks) {
+        float sc[KPS];
+#pragma unroll
+        for (int j = 0; j < KPS; ++j) {
+          sc[j] = w1[j] * h1[j];
+          w1[j] = w2[j];
+          h1[j] = h2[j];
+          w2[j] = w3[j];
+          h2[j] = h3[j];
+        }
+        scales(ks + 3, w3, h3);
         ok = ok && mbar_wait(acc_full + 8 * u, pu, kErrLmEpilogueWait);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         if (any) {
-          const uint32_t at = lane_base + static_cast<uint32_t>(u * C::kN);
-          const float2 s2 = make_float2(sc, sc);
 #pragma unroll
-          for (int c = 0; c < CW; c += 16) {
-            uint32_t d[16];
-            tmem_ld_cols<16>(at + c, d);
-            tmem_ld_wait();
+          for (int j = 0; j < KPS; ++j) {
+            const uint32_t at = lane_base + static_cast<uint32_t>(u * C::kCols + j * C::kN);
+            const float2 s2 = make_float2(sc[j], sc[j]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              acc[c / 2 + j] =
-                  ffma2(make_float2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1])), s2, acc[c / 2 + j]);
+            for (int c = 0; c < CW; c += 16) {
+              uint32_t d[16];
+              tmem_ld_cols<16>(at + c, d);
+              tmem_ld_wait();
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                acc[c / 2 + q] =
+                    ffma2(make_float2(__uint_as_float(d[2 * q]), __uint_as_float(d[2 * q + 1])), s2, acc[c / 2 + q]);
+            }
           }
         }
         tc_fence_before();

@@ -522,7 +522,7 @@ eagle_status_t eagle_lm_head_logits_scaled(int32_t rows, int32_t hidden, int32_t
   CUtensorMap tw, th;
   ScaledParams prm{logits, x_scales, w_scales, rows, vocab, hidden, KB, (rows + 3) / 4 * 4, 0, 0, 0};
   const bool few = rows <= kScFewRows;
-  const int bn = few ? (rows + 15) / 16 * 16 : kScBlock;
+  const int bn = few ? (rows + 15) / 16 * 16 : (rows <= 64 ? 64 : kScBlock);  // rows of a box of x
   if (!encode_bytes(&tw, w, static_cast<uint64_t>(hidden), static_cast<uint64_t>(vocab), kScBlock) ||
       !encode_bytes(&th, x, static_cast<uint64_t>(hidden), static_cast<uint64_t>(rows), static_cast<uint32_t>(bn)))
     return EAGLE_ERR_CUDA;
@@ -534,14 +534,13 @@ eagle_status_t eagle_lm_head_logits_scaled(int32_t rows, int32_t hidden, int32_t
     prm.stages = stages;
     const size_t smem = scaled_smem_bytes(bn, stages);
     const unsigned grid = static_cast<unsigned>(vtiles);
-    if (bn <= 16) return launch_scaled<lm_head_scaled_kernel<8>>(tw, th, prm, grid, kScThreads, smem, st);
-    return launch_scaled<lm_head_scaled_kernel<16>>(tw, th, prm, grid, kScThreads, smem, st);
+    return launch_scaled<lm_head_scaled_kernel>(tw, th, prm, grid, kScThreads, smem, st);
   }
   // two vocabulary blocks a tile (two thirds of the shared-memory bytes per product) while
   // there are six of them per SM, so that the last round of tiles is a small part
   const int row_tiles = (rows + kScBlock - 1) / kScBlock;
   const int64_t wide = (vtiles + 1) / 2 * row_tiles;
-  const int nv = wide >= 6 * kNumSMs ? 2 : 1;
+  const int nv = wide >= 6 * kNumSMs && rows > 64 ? 2 : 1;
   prm.bn = row_tiles;
   prm.stages = static_cast<int32_t>((vtiles + nv - 1) / nv);
   prm.vec = vocab % 4 == 0 && aligned16(logits);
@@ -549,12 +548,16 @@ eagle_status_t eagle_lm_head_logits_scaled(int32_t rows, int32_t hidden, int32_t
   const unsigned grid = static_cast<unsigned>(tiles < kNumSMs ? tiles : kNumSMs);
   if (nv == 2) {
     static const bool shares =
-        register_shares_fit(lm_head_scaled_rows_kernel<2>, kScRowsThreads, kScRowsEpiRegs, kScRowsOtherRegs);
+        register_shares_fit(lm_head_scaled_rows_kernel<2, 128>, kScRowsThreads, kScRowsEpiRegs, kScRowsOtherRegs);
     if (!shares) return EAGLE_ERR_CUDA;
-    return launch_scaled<lm_head_scaled_rows_kernel<2>>(tw, th, prm, grid, kScRowsThreads, ScaledRowsCfg<2>::kAlloc,
-                         st);
+    return launch_scaled<lm_head_scaled_rows_kernel<2, 128>>(tw, th, prm, grid, kScRowsThreads,
+                                                             ScaledRowsCfg<2, 128>::kAlloc, st);
   }
-  return launch_scaled<lm_head_scaled_rows_kernel<1>>(tw, th, prm, grid, kScRowsThreads, ScaledRowsCfg<1>::kAlloc, st);
+  if (rows <= 64)
+    return launch_scaled<lm_head_scaled_rows_kernel<1, 64>>(tw, th, prm, grid, kScRowsThreads,
+                                                            ScaledRowsCfg<1, 64>::kAlloc, st);
+  return launch_scaled<lm_head_scaled_rows_kernel<1, 128>>(tw, th, prm, grid, kScRowsThreads,
+                                                           ScaledRowsCfg<1, 128>::kAlloc, st);
 }
 
 }  // extern "C"
