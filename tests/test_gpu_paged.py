@@ -425,6 +425,7 @@ def test_append_bad_rows_are_skipped_whole(cuda_lib):
     call()
     assert cuda_lib.device_error(reset=True) == 0x206 and (q_out == 7).all()
     pages = cuda_lib.make_pages(c["kp"].shape[0], 16, 1)   # a table of one page a sequence
+    c["table"] = c["table"][:, :1].contiguous()
     call()
     assert cuda_lib.device_error(reset=True) == 0x401 and (q_out == 7).all()
 
@@ -519,6 +520,66 @@ def test_commit(cuda_lib, geom, dtype):
     assert torch.equal(d["kp"].cpu(), t["kp"]) and torch.equal(d["vp"].cpu(), t["vp"])
     assert torch.equal(feat.cpu(), wf)
     assert cuda_lib.device_error(reset=True) == (0x206 if recorded else 0)
+
+
+# ------------------------------------------------------------------ tensors that do not fit
+
+def test_tensors_that_do_not_fit_are_refused(cuda_lib):
+    """Sizes, types and layouts that the shape contradicts never reach the library."""
+    c = _case(14, 2, 3, 4, 2, 64, 16, 0, [40, 20], "bf16")
+    d = {k: v.cuda() for k, v in c.items() if isinstance(v, torch.Tensor)}
+    shape = cuda_lib.make_shape(2, 3, 4, 2, 64, 40, 64, 128, "bf16")
+    pages = cuda_lib.make_pages(d["k_pages"].shape[0], 16, d["table"].shape[1])
+    ws = torch.empty(cuda_lib.paged_workspace_bytes(shape, pages, 0), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(d["q"])
+    args = dict(q=d["q"], k_pages=d["k_pages"], v_pages=d["v_pages"], page_table=d["table"], prefix_lens=d["lens"],
+                shared_len=0, k_tree=d["k_tree"], v_tree=d["v_tree"], parents=d["parents"], out=out, workspace=ws)
+    call = lambda **kw: cuda_lib.tree_attention_paged(shape, pages, **{**args, **kw})
+    call()
+    for name in ("q", "k_pages", "v_pages", "k_tree", "v_tree", "out"):
+        for bad in (args[name].float(), args[name][:1].contiguous(), args[name].cpu(),
+                    args[name].transpose(1, 2)):
+            with pytest.raises(ValueError):
+                call(**{name: bad})
+    for name in ("page_table", "prefix_lens", "parents"):
+        for bad in (args[name].long(), args[name][:1].contiguous(), args[name].cpu()):
+            with pytest.raises(ValueError):
+                call(**{name: bad})
+    with pytest.raises(cuda_lib.EagleError):
+        call(workspace=ws[:256])
+    with pytest.raises(cuda_lib.EagleError):
+        call(workspace=None)
+    with pytest.raises(ValueError):
+        call(workspace=ws.view(torch.float32))
+    with pytest.raises(cuda_lib.EagleError):
+        call(shared_len=41)
+    # rows of an append
+    R = 5
+    q, k = torch.zeros((R, 4, 64), dtype=torch.bfloat16, device="cuda"), torch.zeros((R, 2, 64), dtype=torch.bfloat16,
+                                                                                     device="cuda")
+    pos = torch.zeros((R,), dtype=torch.int32, device="cuda")
+    cs = torch.zeros((40, 64), device="cuda")
+    rope = lambda **kw: cuda_lib.rope_append(shape, pages, **{**dict(
+        q=q, k=k, v=k.clone(), positions=pos, seq_ids=torch.full_like(pos, -1), cos_sin=cs, k_pages=d["k_pages"],
+        v_pages=d["v_pages"], page_table=d["table"], q_out=torch.empty_like(q)), **kw})
+    rope()
+    for kw in (dict(q=q[:4]), dict(q=q.float()), dict(k=k[:, :1]), dict(v=k.transpose(1, 2)), dict(positions=pos[:4]),
+               dict(seq_ids=pos[:4]), dict(positions=pos.long()), dict(cos_sin=cs.double()), dict(cos_sin=cs[0]),
+               dict(q_out=torch.empty_like(q)[:4]), dict(k_out=torch.empty_like(q)), dict(q=q.cpu())):
+        with pytest.raises(ValueError):
+            rope(**kw)
+    with pytest.raises(cuda_lib.EagleError):
+        rope(cos_sin=torch.zeros((40, 72), device="cuda"))       # wider than a head
+    # logits
+    x8 = torch.zeros((3, 256), dtype=torch.float8_e4m3fn, device="cuda")
+    w8, ws8 = torch.zeros((128, 256), dtype=torch.float8_e4m3fn, device="cuda"), torch.ones((1, 2), device="cuda")
+    xs, logits = torch.ones((2, 4), device="cuda"), torch.empty((3, 128), device="cuda")
+    cuda_lib.lm_head_logits_scaled(x8, xs, w8, ws8, logits)
+    cuda_lib.lm_head_logits_scaled(x8.view(torch.uint8), xs, w8.view(torch.uint8), ws8, logits)  # their bytes
+    for bad in ((x8.float(), xs, w8, ws8, logits), (x8, xs[:1], w8, ws8, logits), (x8, xs, w8.half(), ws8, logits),
+                (x8, xs, w8, ws8.double(), logits), (x8, xs, w8, ws8, logits.half()), (x8, xs, w8[:64], ws8, logits)):
+        with pytest.raises(ValueError):
+            cuda_lib.lm_head_logits_scaled(*bad)
 
 
 # ------------------------------------------------------------------ together

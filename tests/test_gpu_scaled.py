@@ -44,20 +44,21 @@ def test_quantize(cuda_lib, rows, cols, dtype):
     assert torch.equal(ws.cpu().double(), scale)
 
 
+@pytest.mark.parametrize("rows", [4, 40, 132])
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
-def test_quantize_keeps_non_finite_blocks_visible(cuda_lib, bad):
-    x = torch.randn(4, 256)
+def test_quantize_keeps_non_finite_blocks_visible(cuda_lib, bad, rows):
+    x = torch.randn(rows, 256)
     x[2, 200] = bad
-    x8 = torch.empty((4, 256), dtype=torch.float8_e4m3fn, device="cuda")
-    xs = torch.empty((2, 4), device="cuda")
+    x8 = torch.empty((rows, 256), dtype=torch.float8_e4m3fn, device="cuda")
+    xs = torch.empty((2, rows), device="cuda")
     cuda_lib.quantize_rows(x.cuda(), x8, xs)
     assert torch.isnan(xs.cpu()).nonzero().tolist() == [[1, 2]]
-    w8, ws = torch.empty_like(x8), torch.empty((1, 2), device="cuda")
+    w8, ws = torch.empty_like(x8), torch.empty((-(-rows // 128), 2), device="cuda")
     cuda_lib.quantize_blocks(x.cuda(), w8, ws)
-    assert torch.isnan(ws.cpu()).tolist() == [[False, True]]
-    logits = torch.empty((4, 4), device="cuda")
+    assert torch.isnan(ws.cpu()).nonzero().tolist() == [[0, 1]]
+    logits = torch.empty((rows, 4), device="cuda")
     y = torch.randn(4, 256)
-    y8, ys = torch.empty_like(x8), torch.empty((1, 2), device="cuda")
+    y8, ys = torch.empty((4, 256), dtype=torch.float8_e4m3fn, device="cuda"), torch.empty((1, 2), device="cuda")
     cuda_lib.quantize_blocks(y.cuda(), y8, ys)
     cuda_lib.lm_head_logits_scaled(x8, xs, y8, ys, logits)
     assert torch.isnan(logits.cpu()).nonzero()[:, 0].unique().tolist() == [2]  # that row alone

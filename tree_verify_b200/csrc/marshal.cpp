@@ -4,8 +4,8 @@
 // spent 8 to 11 us on the host; here it is the checks, one pointer per tensor and the launch.
 //
 // Every function takes the arguments of its namesake in binding.py in order and returns the
-// library's status.  Tensors are dense device tensors of the current device (or None); the
-// structures are the ctypes ones of binding.py.  The library is reached by the addresses
+// library's status.  Tensors are dense device tensors of the current device (or None) of the
+// sizes and types that the shape says; the structures are the ctypes ones of binding.py.  The library is reached by the addresses
 // that bind() is given, so this module links to nothing of it.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -45,29 +45,39 @@ const at::Tensor& tensor(PyObject* o) {
   return t;
 }
 
-// A dense tensor's memory; None is a null pointer.
+// A dense tensor's memory, if it has that many elements of that type; None is a null pointer.
 template <typename T = void>
-T* ptr(PyObject* o) {
+T* ptr(PyObject* o, int64_t numel, at::ScalarType type) {
   if (o == Py_None) return nullptr;
   const at::Tensor& t = tensor(o);
   if (!t.is_contiguous()) throw BadArgument("library arguments are contiguous tensors");
+  if (t.numel() != numel || t.scalar_type() != type)
+    throw BadArgument("a tensor does not have the size or the type that the shape says");
   return static_cast<T*>(t.data_ptr());
+}
+int32_t* ints(PyObject* o, int64_t numel) { return ptr<int32_t>(o, numel, at::kInt); }
+float* floats(PyObject* o, int64_t numel) { return ptr<float>(o, numel, at::kFloat); }
+// e4m3 values, or their bytes
+void* bytes(PyObject* o, int64_t numel) {
+  const bool raw = THPVariable_Check(o) && THPVariable_Unpack(o).scalar_type() == at::kByte;
+  return ptr(o, numel, raw ? at::kByte : at::kFloat8_e4m3fn);
 }
 
 // [R, heads, D] whose rows may be strided parts of a wider array.
 struct Rows {
   void* p = nullptr;
-  int64_t stride = 0, rows = -1;
+  int64_t stride = 0;
 };
-Rows token_rows(PyObject* o) {
+Rows token_rows(PyObject* o, int64_t rows, int64_t heads, int64_t d, at::ScalarType type) {
   Rows r;
   if (o == Py_None) return r;
   const at::Tensor& t = tensor(o);
-  if (t.dim() != 3 || t.stride(2) != 1 || t.stride(1) != t.size(2))
+  if (t.dim() != 3 || t.size(0) != rows || t.size(1) != heads || t.size(2) != d || t.scalar_type() != type)
+    throw BadArgument("token rows are [R, heads, D] of the shape's heads and type");
+  if (rows > 0 && (t.stride(2) != 1 || (heads > 1 && t.stride(1) != d)))
     throw BadArgument("token rows are [R, heads, D] with dense heads");
   r.p = t.data_ptr();
-  r.rows = t.size(0);
-  r.stride = r.rows > 1 ? t.stride(0) : t.size(1) * t.size(2);
+  r.stride = rows > 1 ? t.stride(0) : heads * d;
   return r;
 }
 
@@ -114,6 +124,25 @@ int32_t integer(PyObject* o) {
   if (v < INT32_MIN || v > INT32_MAX) throw BadArgument("a 32-bit integer is expected");
   return static_cast<int32_t>(v);
 }
+
+// What the shape says of the cache.  Its numbers are the library's to refuse; here they only
+// size tensors.
+struct Sizes {
+  int64_t B, N, Hq, Hkv, D, H, pool, table;
+  at::ScalarType type;
+  Sizes(const eagle_shape_t* s, const eagle_pages_t* pg) {
+    if (s == nullptr) throw BadArgument("a shape is expected");
+    B = s->batch;
+    N = s->num_nodes;
+    Hq = s->num_q_heads;
+    Hkv = s->num_kv_heads;
+    D = s->head_dim;
+    H = s->hidden;
+    pool = pg == nullptr ? 0 : static_cast<int64_t>(pg->num_pages) * pg->page_size * Hkv * D;
+    table = pg == nullptr ? 0 : B * pg->max_pages;
+    type = s->dtype == EAGLE_DTYPE_BF16 ? at::kBFloat16 : at::kFloat;
+  }
+};
 
 int32_t dtype(const at::Tensor& t) {
   if (t.scalar_type() == at::kBFloat16) return EAGLE_DTYPE_BF16;
@@ -172,13 +201,12 @@ PyObject* rope_append(PyObject*, Args a, Py_ssize_t n) {
   return guarded(n, 15, [&] {
     const Struct<eagle_shape_t> shape(a[0]);
     const Struct<eagle_pages_t> pages(a[1]);
-    const Rows q = token_rows(a[2]), k = token_rows(a[3]), v = token_rows(a[4]);
+    const Sizes z(shape.p, pages.p);
     const at::Tensor& pos = tensor(a[5]);
-    if (pos.dim() != 1) throw BadArgument("positions are [R]");
-    const int64_t rows = pos.size(0);
-    for (const Rows* r : {&q, &k, &v})
-      if (r->rows >= 0 && r->rows != rows) throw BadArgument("q, k, v and positions have the same number of rows");
-    if (rows > INT32_MAX) throw BadArgument("at most 2^31 - 1 rows");
+    if (pos.dim() != 1 || pos.size(0) > INT32_MAX) throw BadArgument("positions are [R]");
+    const int64_t R = pos.size(0);
+    const Rows q = token_rows(a[2], R, z.Hq, z.D, z.type), k = token_rows(a[3], R, z.Hkv, z.D, z.type),
+               v = token_rows(a[4], R, z.Hkv, z.D, z.type);
     eagle_rope_t rope{0, 0, 0};
     if (a[7] != Py_None) {
       const at::Tensor& cs = tensor(a[7]);
@@ -190,9 +218,11 @@ PyObject* rope_append(PyObject*, Args a, Py_ssize_t n) {
       if (truth < 0) throw PythonError{};
       rope.interleaved = truth;
     }
-    return g_entry.rope_append(shape.p, pages.p, &rope, static_cast<int32_t>(rows), q.p, q.stride, k.p, k.stride, v.p,
-                               v.stride, ptr<int32_t>(a[5]), ptr<int32_t>(a[6]), ptr<float>(a[7]), ptr(a[8]),
-                               ptr(a[9]), ptr<int32_t>(a[10]), ptr(a[11]), ptr(a[12]), stream(a[14]));
+    return g_entry.rope_append(
+        shape.p, pages.p, &rope, static_cast<int32_t>(R), q.p, q.stride, k.p, k.stride, v.p, v.stride, ints(a[5], R),
+        ints(a[6], R), floats(a[7], static_cast<int64_t>(rope.table_len) * rope.rotary_dim), ptr(a[8], z.pool, z.type),
+        ptr(a[9], z.pool, z.type), ints(a[10], z.table), ptr(a[11], R * z.Hq * z.D, z.type),
+        ptr(a[12], R * z.Hkv * z.D, z.type), stream(a[14]));
   });
 }
 
@@ -202,11 +232,15 @@ PyObject* tree_attention_paged(PyObject*, Args a, Py_ssize_t n) {
   return guarded(n, 14, [&] {
     const Struct<eagle_shape_t> shape(a[0]);
     const Struct<eagle_pages_t> pages(a[1]);
-    size_t bytes = 0;
-    if (a[12] != Py_None) bytes = tensor(a[12]).nbytes();
-    return g_entry.tree_attention_paged(shape.p, pages.p, ptr(a[2]), ptr(a[3]), ptr(a[4]), ptr<int32_t>(a[5]),
-                                        ptr<int32_t>(a[6]), integer(a[7]), ptr(a[8]), ptr(a[9]), ptr<int32_t>(a[10]),
-                                        ptr(a[11]), ptr(a[12]), bytes, stream(a[13]));
+    const Sizes z(shape.p, pages.p);
+    const int64_t q = z.B * z.N * z.Hq * z.D, kv = z.B * z.N * z.Hkv * z.D;
+    int64_t space = 0;
+    if (a[12] != Py_None) space = tensor(a[12]).numel();
+    return g_entry.tree_attention_paged(
+        shape.p, pages.p, ptr(a[2], q, z.type), ptr(a[3], z.pool, z.type), ptr(a[4], z.pool, z.type),
+        ints(a[5], z.table), ints(a[6], z.B), integer(a[7]), ptr(a[8], kv, z.type), ptr(a[9], kv, z.type),
+        ints(a[10], z.B * z.N), ptr(a[11], q, z.type), ptr(a[12], space, at::kByte), static_cast<size_t>(space),
+        stream(a[13]));
   });
 }
 
@@ -216,10 +250,12 @@ PyObject* commit_accepted_paged(PyObject*, Args a, Py_ssize_t n) {
   return guarded(n, 15, [&] {
     const Struct<eagle_shape_t> shape(a[0]);
     const Struct<eagle_pages_t> pages(a[1]);
-    return g_entry.commit_accepted_paged(shape.p, pages.p, ptr(a[2]), ptr(a[3]), ptr<int32_t>(a[4]),
-                                         ptr<int32_t>(a[5]), ptr(a[6]), ptr(a[7]), ptr(a[8]), ptr<int32_t>(a[9]),
-                                         ptr<int32_t>(a[10]), ptr<int32_t>(a[11]), ptr<int32_t>(a[12]), ptr(a[13]),
-                                         stream(a[14]));
+    const Sizes z(shape.p, pages.p);
+    const int64_t kv = z.B * z.N * z.Hkv * z.D, rows = z.B * z.N;
+    return g_entry.commit_accepted_paged(
+        shape.p, pages.p, ptr(a[2], z.pool, z.type), ptr(a[3], z.pool, z.type), ints(a[4], z.table), ints(a[5], z.B),
+        ptr(a[6], kv, z.type), ptr(a[7], kv, z.type), ptr(a[8], rows * z.H, z.type), ints(a[9], rows),
+        ints(a[10], rows), ints(a[11], z.B), ints(a[12], z.B), ptr(a[13], rows * z.H, z.type), stream(a[14]));
   });
 }
 
@@ -240,8 +276,9 @@ PyObject* quantize_rows(PyObject*, Args a, Py_ssize_t n) {
     const int64_t R = x.size(0), H = x.size(1);
     if (!is(a[1], R, H) || !is(a[2], (H + 127) / 128, (R + 3) / 4 * 4))
       throw BadArgument("x_out is [R, H] and scales [ceil(H / 128), R rounded up to 4]");
-    return g_entry.quantize_rows(static_cast<int32_t>(R), static_cast<int32_t>(H), dtype(x), ptr(a[0]), ptr(a[1]),
-                                 ptr<float>(a[2]), stream(a[3]));
+    return g_entry.quantize_rows(static_cast<int32_t>(R), static_cast<int32_t>(H), dtype(x),
+                                 ptr(a[0], R * H, x.scalar_type()), bytes(a[1], R * H),
+                                 floats(a[2], (H + 127) / 128 * ((R + 3) / 4 * 4)), stream(a[3]));
   });
 }
 
@@ -253,8 +290,9 @@ PyObject* quantize_blocks(PyObject*, Args a, Py_ssize_t n) {
     const int64_t V = w.size(0), H = w.size(1);
     if (!is(a[1], V, H) || !is(a[2], (V + 127) / 128, (H + 127) / 128))
       throw BadArgument("w_out is [V, H] and scales [ceil(V / 128), ceil(H / 128)]");
-    return g_entry.quantize_blocks(static_cast<int32_t>(V), static_cast<int32_t>(H), dtype(w), ptr(a[0]), ptr(a[1]),
-                                   ptr<float>(a[2]), stream(a[3]));
+    return g_entry.quantize_blocks(static_cast<int32_t>(V), static_cast<int32_t>(H), dtype(w),
+                                   ptr(a[0], V * H, w.scalar_type()), bytes(a[1], V * H),
+                                   floats(a[2], (V + 127) / 128 * ((H + 127) / 128)), stream(a[3]));
   });
 }
 
@@ -271,8 +309,8 @@ PyObject* lm_head_logits_scaled(PyObject*, Args a, Py_ssize_t n) {
           "operands are x [R, H], x_scales [KB, R rounded up to 4], w [V, H], "
           "w_scales [ceil(V / 128), KB] and logits [R, V]");
     return g_entry.lm_head_logits_scaled(static_cast<int32_t>(R), static_cast<int32_t>(H), static_cast<int32_t>(V),
-                                         ptr(a[0]), ptr<float>(a[1]), ptr(a[2]), ptr<float>(a[3]), ptr<float>(a[4]),
-                                         stream(a[5]));
+                                         bytes(a[0], R * H), floats(a[1], KB * ((R + 3) / 4 * 4)), bytes(a[2], V * H),
+                                         floats(a[3], (V + 127) / 128 * KB), floats(a[4], R * V), stream(a[5]));
   });
 }
 

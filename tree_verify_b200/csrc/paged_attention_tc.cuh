@@ -683,9 +683,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
               x[96 + j] = __uint_as_float(v3[j]);
             }
           }
-          // masked scores become -inf, which also drops what a masked place holds
+          // masked scores become -inf, which also drops what a masked place holds (rows that
+          // are not real go on unmasked: nothing reads their P or O but their own lanes)
           const int skip = tree ? 0 : max(0, begin - pos);
-          if (tree || !rvalid || valid < kAttnKeys || skip > 0) {
+          if (tree || valid < kAttnKeys || skip > 0) {
             uint64_t m0 = valid >= 64 ? ~0ull : (1ull << valid) - 1ull;
             uint64_t m1 = valid >= 128 ? ~0ull : (valid <= 64 ? 0ull : (1ull << (valid - 64)) - 1ull);
             if (skip > 0) {
@@ -693,7 +694,6 @@ __global__ void __launch_bounds__(kPgThreads, 1)
               m1 = skip >= 128 ? 0ull : (skip <= 64 ? m1 : m1 & (~0ull << (skip - 64)));
             }
             if (tree) m0 &= tree_bits;
-            if (!rvalid) m0 = m1 = 0ull;
 #pragma unroll
             for (int j = 0; j < 64; ++j) {
               x[j] = ((m0 >> j) & 1ull) ? x[j] : -INFINITY;
@@ -712,7 +712,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           const float m_new = fmaxf(m_ref, fmax3f(mx[0], mx[1], fmaxf(mx[2], mx[3])) * c);
           // the reference moves only when the maximum grows by more than 2^8 over it; P
           // stays below 2^8 and the rescaling of O is rare
-          const bool rebase = m_new != -INFINITY && (m_ref == -INFINITY || m_new > m_ref + kPgRescaleThreshold);
+          const bool rebase =
+              rvalid && m_new != -INFINITY && (m_ref == -INFINITY || m_new > m_ref + kPgRescaleThreshold);
           const bool scale_o = rebase && m_ref != -INFINITY;
           const float f = scale_o ? fast_exp2(m_ref - m_new) : 1.0f;
           if (rebase) {
