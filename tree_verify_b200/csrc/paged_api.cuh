@@ -207,7 +207,8 @@ PagedPlan plan_paged(const eagle_shape_t* s, int32_t shared_len) {
   p.rows_sh = static_cast<int>(B * N < nb ? B * N : nb) * G;
   p.own_row0 = shared_len > 0 ? 2 * (Hkv * ((p.rb_sh + 1) / 2) + kNumSMs) * p.rows_sh : 0;
   p.part_rows = p.own_row0 + 2 * (B * Hkv * ((p.rb_own + 1) / 2) + kNumSMs) * p.rows_own;
-  p.plan_bytes = align256(static_cast<size_t>(2 + B) * sizeof(int64_t));
+  const int64_t items = Hkv * ((p.rb_sh + 1) / 2 + B * ((p.rb_own + 1) / 2));
+  p.plan_bytes = 256 + align256(static_cast<size_t>(items) * sizeof(int2));  // run_shared, cuts
   p.ml_bytes = align256(static_cast<size_t>(p.part_rows) * sizeof(float2));
   p.acc_bytes = align256(static_cast<size_t>(p.part_rows) * s->head_dim * sizeof(float));
   return p;
@@ -224,7 +225,8 @@ eagle_status_t launch_paged_tc(const eagle_shape_t* s, const eagle_pages_t* pg, 
   p.a = ap;
   p.out = static_cast<__nv_bfloat16*>(out);
   uint8_t* w = static_cast<uint8_t*>(ws);
-  p.plan = reinterpret_cast<int64_t*>(w);
+  p.run_shared = reinterpret_cast<int32_t*>(w);
+  p.cuts = reinterpret_cast<int2*>(w + 256);
   p.part_ml = reinterpret_cast<float2*>(w + plan.plan_bytes);
   p.part_acc = reinterpret_cast<float*>(w + plan.plan_bytes + plan.ml_bytes);
   p.NB = plan.nodes_per_tile;
@@ -255,23 +257,32 @@ eagle_status_t launch_paged_tc(const eagle_shape_t* s, const eagle_pages_t* pg, 
       !encode_bf16(&tq, q, 3, qdims, qstrides, qbox) || !encode_bf16(&tkt, kt, 4, tdims, tstrides, tbox) ||
       !encode_bf16(&tvt, vt, 4, tdims, tstrides, tbox))
     return EAGLE_ERR_CUDA;
-  paged_attn_tc_kernel<D><<<kNumSMs, kPgThreads, PgSmem<D>::kAlloc, st>>>(tq, tk, tv, tkt, tvt, p);
-  const eagle_status_t rc = launch_status();
-  if (rc != EAGLE_OK) return rc;
-  // the merge may be launched while the kernel above runs, and waits for it; eight warps
-  // share a row's partials while that does not make more than a few CTAs per SM
-  const int64_t rows = static_cast<int64_t>(ap.B) * ap.N * ap.Hq;
-  const bool split = (rows + 7) / 8 * (D / 16) <= 4 * kNumSMs;
-  const int per = split ? kPgMergeRows<true> : kPgMergeRows<false>;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + per - 1) / per), split ? D / 16 : 1);
-  cfg.blockDim = dim3(split ? 256 : 2 * D);
-  cfg.stream = st;
+  // either kernel may be launched while the one before it on the stream ends, and waits for it
+  // before it touches what that one may
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kNumSMs);
+  cfg.blockDim = dim3(kPgThreads);
+  cfg.dynamicSmemBytes = PgSmem<D>::kAlloc;
+  cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, paged_attn_tc_kernel<D>, tq, tk, tv, tkt, tvt, p) != cudaSuccess) {
+    cudaGetLastError();
+    return EAGLE_ERR_CUDA;
+  }
+  const eagle_status_t rc = launch_status();
+  if (rc != EAGLE_OK) return rc;
+  // the merge: eight warps share a row's partials while that does not make more than a few
+  // CTAs per SM
+  const int64_t rows = static_cast<int64_t>(ap.B) * ap.N * ap.Hq;
+  const bool split = (rows + 7) / 8 * (D / 16) <= 4 * kNumSMs;
+  const int per = split ? kPgMergeRows<true> : kPgMergeRows<false>;
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + per - 1) / per), split ? D / 16 : 1);
+  cfg.blockDim = dim3(split ? 256 : 2 * D);
+  cfg.dynamicSmemBytes = 0;
   const cudaError_t e = split ? cudaLaunchKernelEx(&cfg, paged_attn_merge_kernel<D, true>, p)
                               : cudaLaunchKernelEx(&cfg, paged_attn_merge_kernel<D, false>, p);
   if (e != cudaSuccess) {

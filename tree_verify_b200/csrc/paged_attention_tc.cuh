@@ -43,14 +43,15 @@ constexpr int kPgItems = 2;                   // items described ahead
 constexpr int kPgItemCost = 8;                // units of an item beyond its tiles (see paged_tile_units)
 constexpr float kPgRescaleThreshold = 8.0f;   // log2 units
 constexpr int kPgSoftRegs = 208, kPgOtherRegs = 88;  // of the launch's 168 x 384 registers
-constexpr int kPgPolyPairs = 2;               // of 8 pairs, through the polynomial 2^x
+constexpr int kPgPolyPairs = 1;               // of 8 pairs, through the polynomial 2^x
 
 struct PagedTcParams {
   PagedAttnParams a;
   __nv_bfloat16* out;
   float* part_acc;      // [partial rows, D]: see paged_part_row
   float2* part_ml;      // [partial rows]
-  int64_t* plan;        // [2 + B]: units in all, whether the shared part runs, own start of each sequence
+  int32_t* run_shared;  // whether the shared part runs
+  int2* cuts;           // [items]: the CTAs with an item's first and last tile (see paged_item)
   int32_t NB;           // nodes of a row tile (G * NB <= 128)
   int32_t rb_own, rb_sh;      // row tiles of a sequence, of the batch (0 without a shared part)
   int32_t rows_own, rows_sh;  // rows of a tile that can be real
@@ -95,11 +96,8 @@ __device__ __forceinline__ int64_t paged_div(int64_t a, int64_t b) {
 }
 // Pieces of a line of W units: no more than units, so that none is empty.
 __device__ __forceinline__ int paged_pieces(int64_t W, int ctas) { return W < ctas ? static_cast<int>(W) : ctas; }
-// Piece c is [c W / P, (c + 1) W / P); the CTA whose piece holds unit u.
+// Piece c is [c W / P, (c + 1) W / P).
 __device__ __forceinline__ int64_t paged_cut(int c, int64_t W, int P) { return paged_div(c * W, P); }
-__device__ __forceinline__ int paged_owner(int64_t u, int64_t W, int P) {
-  return static_cast<int>(paged_div((u + 1) * P - 1, W));
-}
 
 // Walks the items of a piece [lo, hi) of the line.
 struct PagedCursor {
@@ -156,15 +154,19 @@ struct PagedCursor {
   }
 };
 
+// Index of an item among the shared or the own ones, and among all (shared ones first).
+__device__ __forceinline__ int64_t paged_item(const PagedTcParams& p, int b, int kvh, int pi) {
+  if (b < 0) return static_cast<int64_t>(kvh) * ((p.rb_sh + 1) >> 1) + pi;
+  return (static_cast<int64_t>(b) * p.a.Hkv + kvh) * ((p.rb_own + 1) >> 1) + pi;
+}
+__device__ __forceinline__ int64_t paged_item_of_all(const PagedTcParams& p, int b, int64_t item) {
+  return b < 0 ? item : static_cast<int64_t>(p.a.Hkv) * ((p.rb_sh + 1) >> 1) + item;
+}
 // Row of the partials where CTA `cta`'s run of an item begins, for group g.  Along the line
 // either the item or the CTA grows from run to run, so item + CTA names a run.
-__device__ __forceinline__ int64_t paged_part_row(const PagedTcParams& p, int b, int kvh, int pi, int cta, int g) {
-  if (b < 0) {
-    const int64_t run = static_cast<int64_t>(kvh) * ((p.rb_sh + 1) >> 1) + pi + cta;
-    return (2 * run + g) * p.rows_sh;
-  }
-  const int64_t run = (static_cast<int64_t>(b) * p.a.Hkv + kvh) * ((p.rb_own + 1) >> 1) + pi + cta;
-  return p.own_row0 + (2 * run + g) * p.rows_own;
+__device__ __forceinline__ int64_t paged_part_row(const PagedTcParams& p, int b, int64_t item, int cta, int g) {
+  if (b < 0) return (2 * (item + cta) + g) * p.rows_sh;
+  return p.own_row0 + (2 * (item + cta) + g) * p.rows_own;
 }
 
 // One CTA's run of an item, as the item warp describes it.
@@ -268,6 +270,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), SM::kTmemCols);
     tmem_relinquish();
   }
+  pdl_wait();  // nothing that another kernel writes is read or written before
   // each thread sums the units of a run of sequences; a block scan gives their starts
   const int chunk = (B + kPgThreads - 1) / kPgThreads;
   const int sb0 = min(B, tid * chunk), sb1 = min(B, sb0 + chunk);
@@ -310,17 +313,13 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   const int P = paged_pieces(W, prm.ctas);
   const int64_t lo = cta < P ? paged_cut(cta, W, P) : W, hi = cta < P ? paged_cut(cta + 1, W, P) : W;
   start += shared_units;
-  if (cta == 0 && tid == 0) {
-    prm.plan[0] = W;
-    prm.plan[1] = run_shared ? 1 : 0;
-  }
+  if (cta == 0 && tid == 0) *prm.run_shared = run_shared ? 1 : 0;
   {
     const int64_t at = max(lo, shared_units);  // the first own unit this CTA may meet
     int64_t u = start;
-    if (sum > 0 && (cta == 0 || (at >= start && at < start + sum))) {
+    if (at >= start && at < start + sum) {
       for (int b = sb0; b < sb1; ++b) {
         const int64_t units = chunk == 1 ? sum : Hkv * paged_head_units(paged_seq(prm, b).n + 1, prm.rb_own);
-        if (cta == 0) prm.plan[2 + b] = u;
         if (at >= u && at < u + units) {
           *first_b_s = b;
           *first_base_s = u;
@@ -402,7 +401,12 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             d.t0 = cur.s.t0;
             d.nrow = cur.nrow();
             d.node0 = 2 * cur.pi * prm.NB;
-            d.prow = paged_part_row(prm, cur.b, cur.kvh, cur.pi, cta, 0);
+            const int64_t item = paged_item(prm, cur.b, cur.kvh, cur.pi);
+            d.prow = paged_part_row(prm, cur.b, item, cta, 0);
+            // for the merge: between the two lie the item's runs
+            int2* cut = prm.cuts + paged_item_of_all(prm, cur.b, item);
+            if (a == 0) cut->x = cta;
+            if (a < z && z == cur.T) cut->y = cta;
           }
         }
         __syncwarp();
@@ -876,14 +880,16 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 // for few rows, the CTA's 8 warps share one such group of columns and take every 8th partial
 // each.  The order of the sums does not depend on timing.
 template <bool kSplit>
-constexpr int kPgMergeRows = kSplit ? 8 : 32;
+constexpr int kPgMergeRows = kSplit ? 8 : 16;
 
 template <int D, bool kSplit>
-__global__ void __launch_bounds__(kSplit ? 256 : 2 * D) paged_attn_merge_kernel(const __grid_constant__ PagedTcParams prm) {
-  constexpr int kBatch = kSplit ? 4 : 6, kRows = kPgMergeRows<kSplit>;
+__global__ void __launch_bounds__(kSplit ? 256 : 2 * D, kSplit ? 1 : 640 / D)
+    paged_attn_merge_kernel(const __grid_constant__ PagedTcParams prm) {
+  constexpr int kBatch = 4, kRows = kPgMergeRows<kSplit>;
   __shared__ int64_t row0_s[2][kRows], out_s[kRows];
   __shared__ int32_t count_s[2][kRows], step_s[2][kRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();  // (a next call's main kernel sets itself up meanwhile)
   pdl_wait();
   if (threadIdx.x < 2 * kRows) {
     // thread = (own or shared runs, row): the first partial's row, the step to the next,
@@ -901,23 +907,19 @@ __global__ void __launch_bounds__(kSplit ? 256 : 2 * D) paged_attn_merge_kernel(
       const int node = in_head / G, hg = in_head - node * G;
       const uint32_t fnode = b * N + node;
       orow = static_cast<int64_t>(fnode) * Hq + kvh * G + hg;
-      // (all of these are on their way before the first is used)
-      const int64_t W = prm.plan[0], shared_runs = prm.plan[1], own_start = prm.plan[2 + b];
-      const PagedSeq s = paged_seq(prm, b);
-      if (k == 0 || (shared_runs != 0 && s.L >= prm.a.shared)) {
-        const int P = paged_pieces(W, prm.ctas);
-        const uint32_t nd = k == 0 ? node : fnode;
-        const int rb = k == 0 ? prm.rb_own : prm.rb_sh;
-        const int rt = nd / static_cast<uint32_t>(prm.NB), pi = rt >> 1;
-        const int nrow = min(2, rb - 2 * pi);
-        const int T = k == 0 ? s.n + 1 : (prm.a.shared + kAttnKeys - 1) / kAttnKeys;
-        const int64_t u0 = (k == 0 ? own_start : 0) + kvh * paged_head_units(T, rb) + paged_pair_units(T, pi);
-        const int c0 = paged_owner(u0, W, P);
-        const int c1 = paged_owner(u0 + static_cast<int64_t>(T - 1) * paged_tile_units(nrow), W, P);
+      const uint32_t nd = k == 0 ? node : fnode;
+      const int rb = k == 0 ? prm.rb_own : prm.rb_sh;
+      if (rb > 0) {
+        const int rt = nd / static_cast<uint32_t>(prm.NB), pi = rt >> 1, nrow = min(2, rb - 2 * pi);
+        const int64_t item = paged_item(prm, k == 0 ? b : -1, kvh, pi);
+        // (all of these are on their way before the first is used; without a shared run the
+        // shared items' cuts are stale, and not taken)
+        const int2 cut = prm.cuts[paged_item_of_all(prm, k == 0 ? b : -1, item)];
+        const int shared_runs = *prm.run_shared, L = prm.a.prefix_lens[b];
         // (of a pair, the second row tile has the second slot)
-        row0 = paged_part_row(prm, k == 0 ? b : -1, kvh, pi, c0, nrow == 2 ? (rt & 1) : 0);
+        row0 = paged_part_row(prm, k == 0 ? b : -1, item, cut.x, nrow == 2 ? (rt & 1) : 0);
         step = 2 * (k == 0 ? prm.rows_own : prm.rows_sh);
-        count = c1 - c0 + 1;
+        count = k == 0 || (shared_runs != 0 && min(L, prm.a.Lmax) >= prm.a.shared) ? cut.y - cut.x + 1 : 0;
         // the row in the tile, below the bits of the partial's first row
         row0 = row0 * 128 + ((nd - rt * prm.NB) * G + hg);
       }
