@@ -4,6 +4,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "lm_head_scaled.cuh"
 #include "paged.cuh"
@@ -118,8 +119,11 @@ bool rotated_out_ok(const void* out, int64_t width, const RowSpan& own, const Ro
 
 // ------------------------------------------------------------------ attention
 
-// The fp32 form: row tiles of 16 rows where no more are in a sequence's kv head, else 64;
-// key tiles divided so that there are about three CTAs for each SM.
+// The fp32 form's row tiles: 4 or 16 rows where no more are in a sequence's kv head (32 tokens
+// of 32/8 heads over 1000 + 0..3000 keys: 4 rows 264 us, 16 rows 372); else 64, or 32 where 64
+// would leave most SMs with a tile or two (three 13-node trees over 333 + 0..300 keys: 32 rows
+// 16.0 us, 64 rows 18.5; eight 64-node trees over 1000 + 0..500: 581 and 492).  Key tiles are
+// divided so that there are about five CTAs for each SM.
 struct PagedF32Plan {
   int rt, splits, tiles_own, tiles_sh;
   int64_t items;
@@ -131,13 +135,17 @@ struct PagedF32Plan {
 PagedF32Plan plan_paged_f32(const eagle_shape_t* s, int32_t shared_len) {
   PagedF32Plan p{};
   const int64_t G = s->num_q_heads / s->num_kv_heads, B = s->batch, N = s->num_nodes, Hkv = s->num_kv_heads;
-  p.rt = N * G <= 16 ? 16 : 64;
-  p.tiles_own = static_cast<int>((N * G + p.rt - 1) / p.rt);
-  p.tiles_sh = shared_len > 0 ? static_cast<int>((B * N * G + p.rt - 1) / p.rt) : 0;
-  p.items = Hkv * (B * p.tiles_own + p.tiles_sh);
+  auto tile = [&](int rt) {
+    p.rt = rt;
+    p.tiles_own = static_cast<int>((N * G + rt - 1) / rt);
+    p.tiles_sh = shared_len > 0 ? static_cast<int>((B * N * G + rt - 1) / rt) : 0;
+    p.items = Hkv * (static_cast<int64_t>(B) * p.tiles_own + p.tiles_sh);
+  };
   const int kt = s->head_dim == 128 ? PagedF32Cfg<128, 64>::kKT : PagedF32Cfg<64, 64>::kKT;
   const int64_t tiles = (static_cast<int64_t>(s->max_prefix_len) + kt - 1) / kt + (N + kt - 1) / kt;
-  int64_t splits = (3 * kNumSMs + p.items - 1) / p.items;
+  tile(N * G <= 4 ? 4 : (N * G <= 16 ? 16 : 64));
+  if (p.rt == 64 && p.items * tiles < 4 * kNumSMs) tile(32);
+  int64_t splits = (5 * kNumSMs + p.items - 1) / p.items;
   if (splits > tiles) splits = tiles;
   p.splits = static_cast<int>(splits);
   const size_t rows = static_cast<size_t>(p.items) * p.splits * p.rt;
@@ -166,19 +174,26 @@ eagle_status_t launch_paged_f32(const PagedF32Plan& plan, const void* q, const v
   p.tiles_own = plan.tiles_own;
   p.tiles_sh = plan.tiles_sh;
   p.direct = plan.direct();
-  paged_attn_f32_kernel<D, RT><<<dim3(static_cast<unsigned>(plan.items), plan.splits), 128, bytes, st>>>(p);
-  const eagle_status_t rc = launch_status();
-  if (rc != EAGLE_OK || p.direct) return rc;
-  const int64_t threads = static_cast<int64_t>(ap.B) * ap.N * ap.Hq * (D / 4);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((threads + 127) / 128));
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
+  // either kernel may be launched while the one before it on the stream ends, and waits for it
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.items), plan.splits);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, paged_attn_f32_kernel<D, RT>, p) != cudaSuccess) {
+    cudaGetLastError();
+    return EAGLE_ERR_CUDA;
+  }
+  const eagle_status_t rc = launch_status();
+  if (rc != EAGLE_OK || p.direct) return rc;
+  const int64_t threads = static_cast<int64_t>(ap.B) * ap.N * ap.Hq * (D / 4);
+  cfg.gridDim = dim3(static_cast<unsigned>((threads + 127) / 128));
+  cfg.dynamicSmemBytes = 0;
   if (cudaLaunchKernelEx(&cfg, paged_attn_f32_merge_kernel<D, RT>, p) != cudaSuccess) {
     cudaGetLastError();
     return EAGLE_ERR_CUDA;
@@ -438,11 +453,18 @@ eagle_status_t eagle_tree_attention_paged(const eagle_shape_t* shape, const eagl
                : launch_paged_tc<128>(shape, pages, p, q, k_pages, v_pages, k_tree, v_tree, out, workspace, st);
   const PagedF32Plan plan = plan_paged_f32(shape, shared_len);
   if (plan.items > INT32_MAX) return EAGLE_ERR_UNSUPPORTED;
-  if (plan.rt == 16)
-    return d64 ? launch_paged_f32<64, 16>(plan, q, k_pages, v_pages, k_tree, v_tree, out, workspace, p, st)
-               : launch_paged_f32<128, 16>(plan, q, k_pages, v_pages, k_tree, v_tree, out, workspace, p, st);
-  return d64 ? launch_paged_f32<64, 64>(plan, q, k_pages, v_pages, k_tree, v_tree, out, workspace, p, st)
-             : launch_paged_f32<128, 64>(plan, q, k_pages, v_pages, k_tree, v_tree, out, workspace, p, st);
+  auto run = [&](auto d, auto rt) {
+    return launch_paged_f32<d(), rt()>(plan, q, k_pages, v_pages, k_tree, v_tree, out, workspace, p, st);
+  };
+  auto with_rows = [&](auto d) {
+    switch (plan.rt) {
+      case 4: return run(d, std::integral_constant<int, 4>());
+      case 16: return run(d, std::integral_constant<int, 16>());
+      case 32: return run(d, std::integral_constant<int, 32>());
+      default: return run(d, std::integral_constant<int, 64>());
+    }
+  };
+  return d64 ? with_rows(std::integral_constant<int, 64>()) : with_rows(std::integral_constant<int, 128>());
 }
 
 eagle_status_t eagle_commit_accepted_paged(const eagle_shape_t* shape, const eagle_pages_t* pages, void* k_pages,

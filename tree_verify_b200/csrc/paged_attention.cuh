@@ -21,11 +21,12 @@ struct PagedAttnParams {
 // shared positions, whose K/V is so read once for kRT rows of any sequences) -- and its key
 // tiles are divided among S CTAs, whose partials (m, l, acc) a second kernel merges.
 //
-// 128 threads: thread (ty, tx) has rows ty + 16 i and, of a tile, keys tx + 8 j in S = Q K^T
-// and columns 4 tx + 32 k in O += P V, so that operands come from shared memory 16 bytes at
-// a time without bank conflicts and a float4 feeds 8 to 13 multiply-adds (16-row tiles: 3.5;
-// those are for the few rows of decoding, where the cache's bytes count).  K and V tiles are
-// double-buffered by asynchronous copies, which fill rows that are not there with zeros.
+// 128 threads: thread (ty, tx) has rows ty + kTY i and, of a tile, keys tx + kTX j in S = Q K^T
+// and columns 4 tx + 4 kTX k in O += P V, so that operands come from shared memory 16 bytes at
+// a time without bank conflicts.  64-row tiles feed 8 to 13 multiply-adds with each float4 (23
+// TFLOP/s); 32 rows give small problems more CTAs, 16 and 4 rows are for single tokens, whose
+// cost is the cache's bytes and the latency of a tile (4 rows: one warp a row).  K and V tiles
+// are double-buffered by asynchronous copies, which fill rows that are not there with zeros.
 
 struct PagedF32Params {
   PagedAttnParams a;
@@ -45,6 +46,8 @@ struct PagedF32Params {
 template <int D, int RT>
 struct PagedF32Cfg {
   static constexpr int kKT = D == 128 ? 32 : 64;  // keys of a tile (16 KB of K)
+  static constexpr int kTY = RT < 16 ? RT : 16;   // threads over the rows, over keys and columns
+  static constexpr int kTX = 128 / kTY;
   static constexpr int kQS = D + 4;               // row strides in floats: 16 bytes past a multiple of 128
   static constexpr int kKS = D + 4;
   static constexpr int kPS = kKT + 4;
@@ -60,7 +63,8 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool i
 template <int D, int RT>
 __global__ void __launch_bounds__(128) paged_attn_f32_kernel(const __grid_constant__ PagedF32Params p) {
   using C = PagedF32Cfg<D, RT>;
-  constexpr int KT = C::kKT, RPT = RT / 16, KPT = KT / 8, CPT = D / 32;
+  constexpr int KT = C::kKT, TX = C::kTX, TY = C::kTY, RPT = RT / TY, KPT = KT / TX;
+  constexpr int CPT = D >= 4 * TX ? D / (4 * TX) : 1;  // (D = 64 leaves half of 32 threads without columns)
   extern __shared__ __align__(16) float f32_smem[];
   float* q_s = f32_smem;
   float* kv_s = q_s + RT * C::kQS;
@@ -69,8 +73,12 @@ __global__ void __launch_bounds__(128) paged_attn_f32_kernel(const __grid_consta
   int32_t* par_s = reinterpret_cast<int32_t*>(anc_s + RT);
   int32_t* live_s = par_s + 64;
   const PagedAttnParams& a = p.a;
-  const int tid = threadIdx.x, ty = tid >> 3, tx = tid & 7;
+  const int tid = threadIdx.x, ty = tid / TX, tx = tid % TX;
+  const bool cols = 4 * tx < D;
   const int N = a.N, G = a.G, Hkv = a.Hkv;
+
+  pdl_launch_dependents();  // the merge waits for this grid
+  pdl_wait();
 
   // ---- the item and its keys
   int64_t it = blockIdx.x;
@@ -203,10 +211,10 @@ __global__ void __launch_bounds__(128) paged_attn_f32_kernel(const __grid_consta
     for (int d = 0; d < D; d += 4) {
       float4 qv[RPT];
 #pragma unroll
-      for (int i = 0; i < RPT; ++i) qv[i] = *reinterpret_cast<const float4*>(q_s + (ty + 16 * i) * C::kQS + d);
+      for (int i = 0; i < RPT; ++i) qv[i] = *reinterpret_cast<const float4*>(q_s + (ty + TY * i) * C::kQS + d);
 #pragma unroll
       for (int j = 0; j < KPT; ++j) {
-        const float4 kv = *reinterpret_cast<const float4*>(ks + (tx + 8 * j) * C::kKS + d);
+        const float4 kv = *reinterpret_cast<const float4*>(ks + (tx + TX * j) * C::kKS + d);
 #pragma unroll
         for (int i = 0; i < RPT; ++i)
           s[i][j] = fmaf(qv[i].w, kv.w, fmaf(qv[i].z, kv.z, fmaf(qv[i].y, kv.y, fmaf(qv[i].x, kv.x, s[i][j]))));
@@ -217,17 +225,17 @@ __global__ void __launch_bounds__(128) paged_attn_f32_kernel(const __grid_consta
     const int end = tree ? N : L;
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-      const uint64_t see = tree ? anc_s[ty + 16 * i] : 0ull;
+      const uint64_t see = tree ? anc_s[ty + TY * i] : 0ull;
       float mx = -INFINITY;
 #pragma unroll
       for (int j = 0; j < KPT; ++j) {
-        const int key = first + tx + 8 * j;
+        const int key = first + tx + TX * j;
         const bool in = key < end && (!tree || ((see >> (key & 63)) & 1ull));
         s[i][j] = in ? s[i][j] * a.scale : -INFINITY;
         mx = fmaxf(mx, s[i][j]);
       }
 #pragma unroll
-      for (int off = 1; off < 8; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      for (int off = 1; off < TX; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
       const float mn = fmaxf(m[i], mx);
       const float base = mn == -INFINITY ? 0.f : mn;  // every key so far is masked
       const float f = expf(m[i] - base);
@@ -236,27 +244,27 @@ __global__ void __launch_bounds__(128) paged_attn_f32_kernel(const __grid_consta
       for (int j = 0; j < KPT; ++j) {
         const float e = expf(s[i][j] - base);
         sum += e;
-        p_s[(ty + 16 * i) * C::kPS + tx + 8 * j] = e;
+        p_s[(ty + TY * i) * C::kPS + tx + TX * j] = e;
       }
 #pragma unroll
-      for (int off = 1; off < 8; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      for (int off = 1; off < TX; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
       l[i] = l[i] * f + sum;
       m[i] = mn;
 #pragma unroll
       for (int k = 0; k < CPT; ++k)
         o[i][k] = make_float4(o[i][k].x * f, o[i][k].y * f, o[i][k].z * f, o[i][k].w * f);
     }
-    __syncwarp();  // a row's weights come from the eight lanes of its ty, all in this warp
+    __syncwarp();  // a row's weights come from the lanes of its ty, all in this warp
 #pragma unroll 2
-    for (int j = 0; j < KT; j += 4) {
+    for (int j = 0; j < KT && cols; j += 4) {
       float4 w[RPT];
 #pragma unroll
-      for (int i = 0; i < RPT; ++i) w[i] = *reinterpret_cast<const float4*>(p_s + (ty + 16 * i) * C::kPS + j);
+      for (int i = 0; i < RPT; ++i) w[i] = *reinterpret_cast<const float4*>(p_s + (ty + TY * i) * C::kPS + j);
 #pragma unroll
       for (int jj = 0; jj < 4; ++jj) {
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
-          const float4 v = *reinterpret_cast<const float4*>(vs + (j + jj) * D + 4 * tx + 32 * k);
+          const float4 v = *reinterpret_cast<const float4*>(vs + (j + jj) * D + 4 * tx + 4 * TX * k);
 #pragma unroll
           for (int i = 0; i < RPT; ++i) {
             const float e = jj == 0 ? w[i].x : (jj == 1 ? w[i].y : (jj == 2 ? w[i].z : w[i].w));
@@ -273,21 +281,22 @@ __global__ void __launch_bounds__(128) paged_attn_f32_kernel(const __grid_consta
   const int64_t part = (static_cast<int64_t>(blockIdx.x) * p.splits + blockIdx.y) * RT;
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
-    const int r = ty + 16 * i;
+    const int r = ty + TY * i;
     if (!row_ok(row0 + r)) continue;
     if (p.direct) {
       const float inv = 1.0f / l[i];  // the node itself is always visible
       float* dst = p.out + row_at(row0 + r);
+      if (!cols) continue;
 #pragma unroll
       for (int k = 0; k < CPT; ++k)
-        *reinterpret_cast<float4*>(dst + 4 * tx + 32 * k) =
+        *reinterpret_cast<float4*>(dst + 4 * tx + 4 * TX * k) =
             make_float4(o[i][k].x * inv, o[i][k].y * inv, o[i][k].z * inv, o[i][k].w * inv);
       continue;
     }
-    if (t0 < t1) {
+    if (t0 < t1 && cols) {
 #pragma unroll
       for (int k = 0; k < CPT; ++k)
-        *reinterpret_cast<float4*>(p.part_acc + (part + r) * D + 4 * tx + 32 * k) = o[i][k];
+        *reinterpret_cast<float4*>(p.part_acc + (part + r) * D + 4 * tx + 4 * TX * k) = o[i][k];
     }
     if (tx == 0) p.part_ml[part + r] = make_float2(m[i], l[i]);
   }
@@ -300,6 +309,7 @@ __global__ void __launch_bounds__(128) paged_attn_f32_merge_kernel(const __grid_
   const PagedAttnParams& a = p.a;
   const int64_t x = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) / (D / 4);
   const int c = (threadIdx.x % (D / 4)) * 4;
+  pdl_launch_dependents();
   pdl_wait();
   if (x >= static_cast<int64_t>(a.B) * a.N * a.Hq) return;
   const int64_t fnode = x / a.Hq;
