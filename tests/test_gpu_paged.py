@@ -121,6 +121,8 @@ ATTN = [
     (2, 17, 8, 8, 128, 64, 1, [1, 2]),
     (9, 64, 32, 8, 64, 64, 1000, [1000 + 37 * i for i in range(9)]),
     (70, 1, 8, 2, 64, 16, 40, [40 + (i * 29) % 200 for i in range(70)]),
+    (4, 64, 8, 2, 128, 256, 0, [63, 64, 65, 192]),              # the tree beside the last keys, or after them
+    (4, 7, 4, 4, 64, 128, 40, [40, 104, 105, 128]),
     (33, 3, 4, 2, 128, 16, 0, [(i * 53) % 300 for i in range(33)]),
 ]
 

@@ -250,7 +250,7 @@ eagle_status_t launch_paged_tc(const eagle_shape_t* s, const eagle_pages_t* pg, 
   p.rows_own = plan.rows_own;
   p.rows_sh = plan.rows_sh;
   p.own_row0 = plan.own_row0;
-  p.box = pg->page_size < kAttnKeys ? pg->page_size : kAttnKeys;
+  p.box = pg->page_size < kHalf ? pg->page_size : kHalf;
   p.ctas = kNumSMs;
   p.scale_log2 = ap.scale * 1.4426950408889634f;
   CUtensorMap tq, tk, tv, tkt, tvt;
@@ -267,7 +267,7 @@ eagle_status_t launch_paged_tc(const eagle_shape_t* s, const eagle_pages_t* pg, 
   // tree K/V viewed as [B][N][Hkv][D]: a box is the node rows of (b, kv head), zeros past N
   const u64 tdims[4] = {Dn, Hkv, N, B};
   const u64 tstrides[3] = {Dn * 2, Hkv * Dn * 2, N * Hkv * Dn * 2};
-  const cuuint32_t tbox[4] = {64, 1, static_cast<cuuint32_t>(kAttnKeys), 1};
+  const cuuint32_t tbox[4] = {64, 1, static_cast<cuuint32_t>(kHalf), 1};
   if (!encode_bf16(&tk, kp, 4, kdims, kstrides, kbox) || !encode_bf16(&tv, vp, 4, kdims, kstrides, kbox) ||
       !encode_bf16(&tq, q, 3, qdims, qstrides, qbox) || !encode_bf16(&tkt, kt, 4, tdims, tstrides, tbox) ||
       !encode_bf16(&tvt, vt, 4, tdims, tstrides, tbox))

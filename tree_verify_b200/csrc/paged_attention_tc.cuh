@@ -21,7 +21,8 @@
 // scores S and accumulator O in TMEM and its own chain S = Q K^T, softmax, O += P V; one
 // group's softmax runs under the other's MMAs.  With two row tiles in the item the groups
 // take one each and share every K/V tile; with one, they take the even and the odd tiles of
-// the CTA's run and add up their sums at its end.
+// the CTA's run and add up their sums at the end of an item (an item of one tile is one
+// group's alone, and the next item the other's).
 //
 //   warps 0-3, 4-7   softmax groups 0 and 1
 //   warp 8           TMA of the K and V tiles: one box per page and 64 columns, a lane each
@@ -39,6 +40,7 @@ namespace eagle {
 constexpr int kPgThreads = 32 * 12;
 constexpr int kPgLoadWarp = 8, kPgMmaWarp = 9, kPgItemWarp = 11;
 constexpr int kPgReaders = 11;                // readers of an item: 8 softmax warps, the loads, 2 MMA issuers
+constexpr int kHalf = kAttnKeys / 2;          // keys of half a tile; rows that a tree has at most
 constexpr int kPgItems = 2;                   // items described ahead
 constexpr int kPgItemCost = 8;                // units of an item beyond its tiles (see paged_tile_units)
 constexpr float kPgRescaleThreshold = 8.0f;   // log2 units
@@ -56,7 +58,7 @@ struct PagedTcParams {
   int32_t rb_own, rb_sh;      // row tiles of a sequence, of the batch (0 without a shared part)
   int32_t rows_own, rows_sh;  // rows of a tile that can be real
   int64_t own_row0;           // first partial row of the own part
-  int32_t box;          // rows of a TMA box: min(page size, 128)
+  int32_t box;          // rows of a TMA box: min(page size, 64)
   int32_t ctas;         // pieces of the line of units
   float scale_log2;
 };
@@ -66,7 +68,8 @@ struct PagedSeq {
   int32_t L;      // its length, clamped
   int32_t begin;  // first own position
   int32_t t0;     // position of tile 0's first key (begin, rounded down to a box)
-  int32_t n;      // key tiles (the tree tile comes after them)
+  int32_t T;      // tiles: of the keys, and of the tree, which takes the upper half of the last
+                  // key tile where that one leaves it free, else a tile of its own
 };
 __device__ __forceinline__ PagedSeq paged_seq(const PagedTcParams& p, int b) {
   PagedSeq s;
@@ -74,7 +77,8 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedTcParams& p, int b) {
   s.L = L < 0 ? 0 : (L > p.a.Lmax ? p.a.Lmax : L);
   s.begin = s.L >= p.a.shared ? p.a.shared : 0;
   s.t0 = s.begin & ~(p.box - 1);
-  s.n = s.L > s.begin ? (s.L - s.t0 + kAttnKeys - 1) / kAttnKeys : 0;
+  const int keys = s.L > s.begin ? s.L - s.t0 : 0;
+  s.T = (keys + kAttnKeys / 2 + kAttnKeys - 1) / kAttnKeys;
   return s;
 }
 
@@ -111,7 +115,7 @@ struct PagedCursor {
     rb = p.rb_own;
     if (b < p.a.B) {
       s = paged_seq(p, b);
-      T = s.n + 1;
+      T = s.T;
     }
   }
   // at unit lo; first_b, first_base: the own sequence that holds lo (or sequence 0) and its start
@@ -124,7 +128,7 @@ struct PagedCursor {
       T = (p.a.shared + kAttnKeys - 1) / kAttnKeys;
       s.L = p.a.shared;
       s.begin = s.t0 = 0;
-      s.n = T;
+      s.T = T;
     } else {
       b = first_b;
       base = first_base;
@@ -174,7 +178,7 @@ struct PagedRun {
   int32_t b;       // sequence, -1 in the shared part, kPgEnd after the last item
   int32_t kvh;
   int32_t a, z;    // tiles [a, z); none when no tile starts in the piece
-  int32_t n;       // index of the tree tile (none in the shared part)
+  int32_t n;       // index of the tile with the tree, the last (none in the shared part)
   int32_t L, begin, t0;
   int32_t nrow;    // row tiles: 2, or 1 whose key tiles the groups take in turn
   int32_t node0;   // first node of row tile 0, in the sequence or (shared) in the batch
@@ -278,7 +282,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   int first_long = INT32_MAX;  // a sequence that holds the whole shared part
   for (int b = sb0; b < sb1; ++b) {
     const PagedSeq s = paged_seq(prm, b);
-    sum += Hkv * paged_head_units(s.n + 1, prm.rb_own);
+    sum += Hkv * paged_head_units(s.T, prm.rb_own);
     if (s.L >= prm.a.shared) first_long = min(first_long, b);
     if (cta == 0) {
       const int raw = prm.a.prefix_lens[b];
@@ -319,7 +323,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     int64_t u = start;
     if (at >= start && at < start + sum) {
       for (int b = sb0; b < sb1; ++b) {
-        const int64_t units = chunk == 1 ? sum : Hkv * paged_head_units(paged_seq(prm, b).n + 1, prm.rb_own);
+        const int64_t units = chunk == 1 ? sum : Hkv * paged_head_units(paged_seq(prm, b).T, prm.rb_own);
         if (at >= u && at < u + units) {
           *first_b_s = b;
           *first_base_s = u;
@@ -395,7 +399,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             d.kvh = cur.kvh;
             d.a = a;
             d.z = z;
-            d.n = cur.b < 0 ? INT32_MAX : cur.s.n;
+            d.n = cur.b < 0 ? INT32_MAX : cur.T - 1;
             d.L = cur.s.L;
             d.begin = cur.s.begin;
             d.t0 = cur.s.t0;
@@ -449,26 +453,26 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           record_error(kErrPageIndex);
           return prm.a.map.num_pages;
         };
-        const int zk = min(z, n);  // key tiles end here; the tree tile may follow
         const int per = 32 / boxes;  // tiles of a group
-        int ent = 0, ent_next = a < zk ? fetch(a) : 0, k = 0;
+        int ent = 0, ent_next = fetch(a), k = 0;
         for (int t = a; t < z; ++t) {
-          if (k == 0 && t < zk) {
+          if (k == 0) {
             ent = ent_next;
-            ent_next = t + per < zk ? fetch(t + per) : 0;
+            ent_next = t + per < z ? fetch(t + per) : 0;
           }
+          // boxes of keys in this tile: none of the half that the tree takes
+          const int tree_row = t == n ? (L > t0 + t * kAttnKeys ? kHalf : 0) : kAttnKeys;
           const int pg = __shfl_sync(0xffffffffu, ent, (k * boxes + bc) & 31);
           const int at = (t0 + t * kAttnKeys + bc * box) & page_mask;
           if (++k == per) k = 0;
           auto issue = [&](uint32_t fb, uint32_t dst, const CUtensorMap* map, const CUtensorMap* tree) {
             if (lane == 0) mbar_arrive_expect_tx(fb, SM::kTile);
             __syncwarp();
-            if (t < n) {
-              if (bc < boxes)
-                tma_load_4d(dst + bh * kAttnKeys * 128 + bc * box * 128, map, fb, bh * 64, at, kvh, pg);
-            } else if (bc == 0) {
-              tma_load_4d(dst + bh * kAttnKeys * 128, tree, fb, bh * 64, kvh, 0, b);
-            }
+            if (bc * box < tree_row)
+              tma_load_4d(dst + bh * kAttnKeys * 128 + bc * box * 128, map, fb, bh * 64, at, kvh, pg);
+            else if (t == n && (bc == boxes || (bc == boxes + 1 && tree_row == 0)))  // (nodes past 63: zeros)
+              tma_load_4d(dst + bh * kAttnKeys * 128 + (tree_row + (bc - boxes) * kHalf) * 128, tree, fb, bh * 64,
+                          kvh, (bc - boxes) * kHalf, b);
           };
           if (issued_k >= SK) ok = mbar_wait(k_empty + 8 * sk, pk, kErrAttnProducerWait);
           ok = __all_sync(0xffffffffu, ok);
@@ -650,10 +654,11 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       for (int t = t_first; t < z; t += step, ++n) {
         const bool tree = t == tree_t;
         const int pos = t0 + t * kAttnKeys;
-        const int valid = tree ? N : min(kAttnKeys, L - pos);
+        const int valid = max(0, min(kAttnKeys, L - pos));  // keys of the cache in this tile
+        const bool upper = tree ? valid > 0 : valid > kHalf;  // whether its upper half is used
         wait(s_full + 8 * g, n & 1);
         tc_fence_after();
-        if (!tree && valid < kAttnKeys) {
+        if (valid > 0 && valid < kAttnKeys) {
           // what the last page holds past the length must not reach P V, whatever it is:
           // zero those rows of the V slot once it has landed (later boxes came in as zeros).
           // The slot's tile before this one has landed -- the issuer saw it before this S --
@@ -689,15 +694,17 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           }
           // masked scores become -inf, which also drops what a masked place holds (rows that
           // are not real go on unmasked: nothing reads their P or O but their own lanes)
-          const int skip = tree ? 0 : max(0, begin - pos);
+          const int skip = max(0, begin - pos);
           if (tree || valid < kAttnKeys || skip > 0) {
             uint64_t m0 = valid >= 64 ? ~0ull : (1ull << valid) - 1ull;
             uint64_t m1 = valid >= 128 ? ~0ull : (valid <= 64 ? 0ull : (1ull << (valid - 64)) - 1ull);
-            if (skip > 0) {
-              m0 = skip >= 64 ? 0ull : m0 & (~0ull << skip);
-              m1 = skip >= 128 ? 0ull : (skip <= 64 ? m1 : m1 & (~0ull << (skip - 64)));
+            if (skip > 0) m0 = skip >= 64 ? 0ull : m0 & (~0ull << skip);  // (tiles start less than 64 keys before)
+            if (tree) {
+              if (upper)
+                m1 = tree_bits;
+              else
+                m0 = tree_bits;
             }
-            if (tree) m0 &= tree_bits;
 #pragma unroll
             for (int j = 0; j < 64; ++j) {
               x[j] = ((m0 >> j) & 1ull) ? x[j] : -INFINITY;
@@ -742,6 +749,13 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t w[32];
+            if (h == 1 && !upper) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) w[e] = 0u;
+              tmem_st_cols<32>(s_col + 32, w);
+              tmem_st_wait();
+              break;
+            }
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const float2 y = ffma2(make_float2(x[64 * h + 2 * e], x[64 * h + 2 * e + 1]), make_float2(c, c),
@@ -799,6 +813,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         }
       };
       const bool any = nrow == 2 ? z > a : z > t_first;  // this group took a tile
+      const bool meet = nrow == 1 && z - a > 1;           // both did, of the same rows
       if (any) {
         wait(pv_done + 8 * g, (n - 1) & 1);
         tc_fence_after();
@@ -807,7 +822,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       // same rows, count for
       float w0 = direct ? 1.0f / l : 1.0f, w1 = 0.f;
       int c0 = 0, c1 = D;
-      if (nrow == 1) {
+      if (meet) {
         // the sums meet here: both O are in this warp's TMEM lanes, and each group brings half
         // of the columns out
         if (g == 1) xch[r] = make_float2(m_ref, l);
@@ -835,7 +850,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         c0 = g * (D / 2);
         c1 = c0 + D / 2;
       }
-      if (live && z > a) {
+      if (live && any) {
         const uint32_t other = lane_base + SM::kOCol + (g ^ 1) * D;
 #pragma unroll 1
         for (int cc = c0; cc < c1; cc += 16) {
@@ -845,18 +860,20 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           tmem_ld_cols<16>(o_col + cc, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = w0 > 0.f ? __uint_as_float(o[k]) * w0 : 0.f;
-          if (nrow == 1) {
+          for (int k = 0; k < 16; ++k) v[k] = w0 != 0.f ? __uint_as_float(o[k]) * w0 : 0.f;
+          if (meet) {
             tmem_ld_cols<16>(other + cc, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] += w1 > 0.f ? __uint_as_float(o[k]) * w1 : 0.f;
+            for (int k = 0; k < 16; ++k) v[k] += w1 != 0.f ? __uint_as_float(o[k]) * w1 : 0.f;
           }
           put(cc, v);
         }
       }
-      if (rvalid && !direct && (nrow == 2 || g == 0)) prm.part_ml[prow + r] = make_float2(m_ref, l);
-      if (nrow == 1) {  // neither group lets its next P V at its O before the other has read it
+      // (an empty run's partial says so)
+      if (rvalid && !direct && (nrow == 2 || (meet || z == a ? g == 0 : any)))
+        prm.part_ml[prow + r] = make_float2(m_ref, l);
+      if (meet) {  // neither group lets its next P V at its O before the other has read it
         tc_fence_before();
         both_sync();
       }
