@@ -414,9 +414,11 @@ eagle_status_t eagle_rope_append(const eagle_shape_t *shape, const eagle_pages_t
  *                those sequences.  A sequence shorter than shared_len (a padding entry of
  *                length 0, say) reads all its positions through its own table row.
  *   workspace    >= eagle_paged_workspace_bytes(shape, pages, shared_len), 256-byte aligned
- * Positions past a sequence's length are never used, whatever they hold.  A needed position
- * on a page outside [0, num_pages) counts as a zero key and value.
- * max_prefix_len <= max_pages * page_size.  Calls that may overlap need workspaces of their
+ * Positions past a sequence's length are never used, whatever they hold, nor are the keys of
+ * nodes that a node does not see.  Values are not masked but weighted by 0: an infinity or a
+ * NaN in a node's v_tree reaches every node of its tree.  A needed position on a page outside
+ * [0, num_pages) counts as a zero key and value.
+ * max_prefix_len <= max_pages * page_size and < 2^31 - 512.  out overlaps no input.  Calls that may overlap need workspaces of their
  * own, graphs that may run at the same time too.
  */
 size_t eagle_paged_workspace_bytes(const eagle_shape_t *shape, const eagle_pages_t *pages,
@@ -433,7 +435,7 @@ eagle_status_t eagle_tree_attention_paged(const eagle_shape_t *shape, const eagl
  * of the accepted path.  Arguments and outputs as there; the cache's capacity is
  * max_pages * page_size, and new_prefix_lens[b] is -1 too (nothing written, device error
  * 0x206) when one of the n positions has no page in the pool.  Sequences must not share the
- * pages that receive new rows.
+ * pages that receive new rows.  feat must not overlap hidden.
  */
 eagle_status_t eagle_commit_accepted_paged(const eagle_shape_t *shape, const eagle_pages_t *pages,
                                            void *k_pages, void *v_pages,
@@ -454,7 +456,8 @@ eagle_status_t eagle_commit_accepted_paged(const eagle_shape_t *shape, const eag
  *   x_scales  [KB, ldm] fp32 with ldm = R rounded up to a multiple of 4 (entries past R unused)
  *   w_scales  [ceil(V / 128), KB] fp32
  *   logits    [R, V] fp32
- * Any fp32 scales are taken; eagle_quantize_rows / eagle_quantize_blocks make them from dtype
+ * Any fp32 scales are taken whose products x_scales * w_scales, which are formed first, are
+ * finite.  No output overlaps an input or another output.  eagle_quantize_rows / eagle_quantize_blocks make them from dtype
  * (eagle_dtype_t) values: per block the power of two 2^e with the smallest e >= -126 for which
  * the block's largest magnitude is <= 448 * 2^e, elements rounded to nearest even after an
  * exact division by it.  A block that holds an infinity or a NaN gets a NaN scale.  R = 0 is

@@ -2,6 +2,10 @@
 
 Pools are filled with NaN wherever no sequence keeps a position, and table entries past a
 sequence's length hold indices far outside the pool: neither may reach an output."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -10,6 +14,7 @@ import workloads as wl
 from tests import paged_ref as ref
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 JUNK = (-1, 1 << 30, -(1 << 31), 123456789)
 
 
@@ -248,6 +253,73 @@ def test_attention_ragged_batch_repeats(cuda_lib):
             junk.fill_(i)
         call()
         assert torch.equal(out, first), i
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shared", [0, 40])
+def test_attention_nan_reaches_those_that_see_it(cuda_lib, dtype, shared):
+    """A NaN in one key: every output that sees the key is NaN, wherever it falls in a tile
+    and though it may be alone in its part; all others are as without it."""
+    clean = _case(14, 3, 9, 4, 2, 64, 16, shared, [300, 0, 41], dtype)
+    _, out, call, guards = _launcher(cuda_lib, clean)
+    call()
+    guards()
+    _check(clean, out)
+    keys = [("prefix", 0, 45), ("prefix", 0, 128), ("prefix", 0, 299), ("prefix", 2, 40)]
+    keys += [("prefix", 0, j) for j in range(130, 150)] + [("tree", b, i) for b in range(3) for i in range(9)]
+    for kind, b, i in keys:
+        c = {k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in clean.items()}
+        hit = torch.zeros(out.shape, dtype=torch.bool)
+        if kind == "tree":
+            c["k_tree"][b, i, 1] = float("nan")
+            hit[b, :, 2:] = ref.visible(c["parents"][b].tolist())[:, i, None, None]
+        else:
+            c["k_pages"][c["table"][b, i // 16], 1, i % 16] = float("nan")
+            hit[b, :, 2:] = True
+        _, got, call, guards = _launcher(cuda_lib, c)
+        call()
+        guards()
+        assert torch.equal(torch.isnan(got).cpu(), hit), (kind, b, i)
+        assert torch.equal(got[~hit.cuda()], out[~hit.cuda()]), (kind, b, i)
+
+
+FIRST_CALL = """
+import sys
+import torch
+from tests import test_gpu_paged as t
+from tree_verify_b200 import binding
+dtype = sys.argv[1]
+c = t._case(15, 2, 9, 4, 2, 128, 16, 30, [300, 31], dtype)
+_, out, call, guards = t._launcher(binding, c)
+x = torch.randn((33, 256), device="cuda")
+w = torch.randn((300, 256), device="cuda")
+e4m3 = torch.float8_e4m3fn
+x8, w8 = torch.empty(x.shape, dtype=e4m3, device="cuda"), torch.empty(w.shape, dtype=e4m3, device="cuda")
+xs, ws = torch.empty((2, 36), device="cuda"), torch.empty((3, 2), device="cuda")
+logits = torch.empty((33, 300), device="cuda")
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    call()
+    binding.quantize_blocks(w, w8, ws)
+    binding.quantize_rows(x, x8, xs)
+    binding.lm_head_logits_scaled(x8, xs, w8, ws, logits)
+for _ in range(2):
+    graph.replay()
+guards()
+t._check(c, out)
+first = logits.clone()
+binding.lm_head_logits_scaled(x8, xs, w8, ws, logits)
+torch.cuda.synchronize()
+assert torch.equal(first, logits) and torch.isfinite(logits).all()
+assert binding.device_error(reset=True) == 0
+"""
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_first_calls_of_a_process_may_be_captured(dtype):
+    done = subprocess.run([sys.executable, "-c", FIRST_CALL, dtype], cwd=ROOT, capture_output=True, text=True,
+                          timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 def test_attention_two_calls_at_once(cuda_lib):

@@ -89,6 +89,19 @@ def test_attention_workspace(lib, shared):
     assert binding.paged_workspace_bytes(_shape(), _pages(), 501) == 0
 
 
+def test_attention_overlaps_and_longest_cache(lib):
+    p = [FAKE + (i << 20) for i in range(9)]
+    rows = 2 * 13 * 128 * 2
+    for i, n in ((0, rows * 8), (5, rows * 2), (6, rows * 2)):              # q, k_tree, v_tree
+        for at in (0, n - 16, 16 - rows * 8):
+            x = list(p)
+            x[8] = x[i] + at
+            assert _attend(lib, ptrs=x) == INVALID, (i, at)
+    wide = dict(size=256, width=(1 << 23) - 1)
+    assert binding.paged_workspace_bytes(_shape(max_prefix_len=(1 << 31) - 513), _pages(**wide), 0) > 0
+    assert binding.paged_workspace_bytes(_shape(max_prefix_len=(1 << 31) - 512), _pages(**wide), 0) == 0
+
+
 # ------------------------------------------------------------------ append
 
 def _append(lib, s=None, pg=None, rope=(600, 64, 0), rows=7, **kw):
@@ -157,6 +170,9 @@ def test_commit_bad_arguments(lib):
     p = [FAKE + (j << 16) for j in range(12)]
     p[10] = p[3] + 4  # new_prefix_lens overlaps prefix_lens
     assert _commit(lib, ptrs=p) == INVALID
+    p = [FAKE + (j << 16) for j in range(12)]
+    p[11] = p[6] + 2 * 13 * 512 * 2 - 16  # feat overlaps hidden
+    assert _commit(lib, ptrs=p) == INVALID
 
 
 # ------------------------------------------------------------------ e4m3
@@ -171,6 +187,9 @@ def test_quantize_bad_arguments(lib, name):
         a[i] = v
         assert f(*a) == INVALID, (i, v)
     assert f(0, 256, 1, None, None, None, None) == 0
+    x, x8, sc = FAKE, FAKE + (1 << 16), FAKE + (2 << 16)
+    for bad in ((x, x, sc), (x, x + 2032, sc), (x, x8, x8), (x, x8, x8 + 1008), (x, x8, x)):  # 4 x 256 bf16
+        assert f(4, 256, 1, *bad, None) == INVALID, bad
 
 
 def test_scaled_logits_bad_arguments(lib):
@@ -182,6 +201,10 @@ def test_scaled_logits_bad_arguments(lib):
         a[i] = v
         assert f(*a) == INVALID, (i, v)
     assert f(0, 256, 100, None, None, None, None, None, None) == 0
+    p = [FAKE + (j << 20) for j in range(5)]
+    for i, n in enumerate((4 * 256, 2 * 4 * 4, 100 * 256, 2 * 4)):          # logits over x, scales, w, scales
+        for at in (0, n - 4, 4 - 4 * 100 * 4):
+            assert f(4, 256, 100, *p[:4], p[i] + at, None) == INVALID, (i, at)
     assert f((1 << 24) + 1, 256, 100, FAKE, FAKE, FAKE, FAKE, FAKE, None) == UNSUPPORTED
     assert f(4, 256, 65536 * 128, FAKE, FAKE, FAKE, FAKE, FAKE, None) == UNSUPPORTED
 

@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kScThreads, 2)
       if (any) {
 #pragma unroll
         for (int j = 0; j < kScCW / 4; ++j) {
-          const float4 h4 = __ldg(hs + min(col0 / 4 + j, last4));
+          const float4 h4 = hs[min(col0 / 4 + j, last4)];
           const float2 s0 = fmul2(make_float2(h4.x, h4.y), make_float2(w, w));
           const float2 s1 = fmul2(make_float2(h4.z, h4.w), make_float2(w, w));
           acc[2 * j] = ffma2(make_float2(__uint_as_float(d[4 * j]), __uint_as_float(d[4 * j + 1])), s0, acc[2 * j]);
@@ -523,8 +523,8 @@ __global__ void __launch_bounds__(kScRowsThreads, 1)
           const int kb = ks * KPS + j;
           w[j] = h[j] = 0.f;
           if (kb < KB) {
-            w[j] = __ldg(wsv + kb);
-            h[j] = __ldg(hsv + static_cast<size_t>(kb) * prm.ldm);
+            w[j] = wsv[kb];
+            h[j] = hsv[static_cast<size_t>(kb) * prm.ldm];
           }
         }
       };

@@ -38,6 +38,8 @@ eagle_status_t check_paged_shape(const eagle_shape_t* s, const eagle_pages_t* pg
   if (rc != EAGLE_OK) return rc;
   if (static_cast<int64_t>(pg->max_pages) * pg->page_size < s->max_prefix_len) return EAGLE_ERR_INVALID_ARGUMENT;
   if (shared_len < 0 || shared_len > s->max_prefix_len) return EAGLE_ERR_INVALID_ARGUMENT;
+  // positions, rounded up to tiles, are 32-bit
+  if (s->max_prefix_len > INT32_MAX - 512) return EAGLE_ERR_INVALID_ARGUMENT;
   return EAGLE_OK;
 }
 
@@ -344,6 +346,12 @@ eagle_status_t launch_scaled(const CUtensorMap& tw, const CUtensorMap& th, const
   return launch_status();
 }
 
+// A quantiser's values, e4m3 values and scales share no byte.
+bool quantized_apart(const void* x, const void* x8, const float* scales, size_t n, int32_t dtype, size_t scale_bytes) {
+  const size_t in = n * (dtype == EAGLE_DTYPE_F32 ? 4 : 2);
+  return !overlap(x, in, x8, n) && !overlap(x, in, scales, scale_bytes) && !overlap(x8, n, scales, scale_bytes);
+}
+
 bool dtype_ok(int32_t dtype) { return dtype == EAGLE_DTYPE_F32 || dtype == EAGLE_DTYPE_BF16; }
 
 }  // namespace
@@ -434,6 +442,11 @@ eagle_status_t eagle_tree_attention_paged(const eagle_shape_t* shape, const eagl
                               workspace_bytes, eagle_paged_workspace_bytes(shape, pages, shared_len));
   if (rc != EAGLE_OK) return rc;
   if (page_table == nullptr) return EAGLE_ERR_INVALID_ARGUMENT;
+  // queries and tree are read by some CTAs while others write outputs
+  const size_t row = static_cast<size_t>(shape->batch) * shape->num_nodes * shape->head_dim * elem_size(shape);
+  const size_t qn = row * shape->num_q_heads, tn = row * shape->num_kv_heads;
+  if (overlap(out, qn, q, qn) || overlap(out, qn, k_tree, tn) || overlap(out, qn, v_tree, tn))
+    return EAGLE_ERR_INVALID_ARGUMENT;
   PagedAttnParams p{};
   p.map = page_map(pages, page_table);
   p.prefix_lens = prefix_lens;
@@ -479,6 +492,8 @@ eagle_status_t eagle_commit_accepted_paged(const eagle_shape_t* shape, const eag
   if (rc != EAGLE_OK) return rc;
   if (page_table == nullptr) return EAGLE_ERR_INVALID_ARGUMENT;
   const int esize = elem_size(shape);
+  const size_t hn = static_cast<size_t>(shape->batch) * shape->num_nodes * shape->hidden * esize;
+  if (overlap(feat, hn, hidden, hn)) return EAGLE_ERR_INVALID_ARGUMENT;  // (a gather)
   CommitPagedParams p{};
   p.k_pages = static_cast<uint8_t*>(k_pages);
   p.v_pages = static_cast<uint8_t*>(v_pages);
@@ -508,6 +523,9 @@ eagle_status_t eagle_quantize_rows(int32_t rows, int32_t cols, int32_t dtype, co
   if (!aligned16(x) || !aligned16(x_out) || !aligned16(scales)) return EAGLE_ERR_INVALID_ARGUMENT;
   if (rows > INT32_MAX - 3) return EAGLE_ERR_INVALID_ARGUMENT;
   const int kblocks = (cols + kScBlock - 1) / kScBlock, ldm = (rows + 3) / 4 * 4;
+  if (!quantized_apart(x, x_out, scales, static_cast<size_t>(rows) * cols, dtype,
+                       static_cast<size_t>(kblocks) * ldm * sizeof(float)))
+    return EAGLE_ERR_INVALID_ARGUMENT;
   const int64_t grid = (static_cast<int64_t>(rows) * kblocks + 3) / 4;
   if (grid > INT32_MAX) return EAGLE_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -528,6 +546,8 @@ eagle_status_t eagle_quantize_blocks(int32_t rows, int32_t cols, int32_t dtype, 
     return EAGLE_ERR_INVALID_ARGUMENT;
   const int kblocks = (cols + kScBlock - 1) / kScBlock;
   const int64_t grid = (static_cast<int64_t>(rows) + kScBlock - 1) / kScBlock * kblocks;
+  if (!quantized_apart(w, w_out, scales, static_cast<size_t>(rows) * cols, dtype, grid * sizeof(float)))
+    return EAGLE_ERR_INVALID_ARGUMENT;
   if (grid > INT32_MAX) return EAGLE_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == EAGLE_DTYPE_F32)
@@ -551,6 +571,12 @@ eagle_status_t eagle_lm_head_logits_scaled(int32_t rows, int32_t hidden, int32_t
   const int64_t vtiles = (static_cast<int64_t>(vocab) + kScBlock - 1) / kScBlock;
   if (rows > (1 << 24) || vtiles > 65535) return EAGLE_ERR_UNSUPPORTED;
   const int KB = (hidden + kScBlock - 1) / kScBlock;
+  const size_t out_bytes = static_cast<size_t>(rows) * vocab * sizeof(float);
+  if (overlap(logits, out_bytes, x, static_cast<size_t>(rows) * hidden) ||
+      overlap(logits, out_bytes, w, static_cast<size_t>(vocab) * hidden) ||
+      overlap(logits, out_bytes, x_scales, static_cast<size_t>(KB) * ((rows + 3) / 4 * 4) * sizeof(float)) ||
+      overlap(logits, out_bytes, w_scales, static_cast<size_t>(vtiles) * KB * sizeof(float)))
+    return EAGLE_ERR_INVALID_ARGUMENT;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   CUtensorMap tw, th;
   ScaledParams prm{logits, x_scales, w_scales, rows, vocab, hidden, KB, (rows + 3) / 4 * 4, 0, 0, 0};

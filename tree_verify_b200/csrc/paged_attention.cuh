@@ -343,14 +343,14 @@ __global__ void __launch_bounds__(128) paged_attn_f32_merge_kernel(const __grid_
     float mn = m;
 #pragma unroll
     for (int k = 0; k < 8; ++k) mn = fmaxf(mn, ml[k].x);
-    if (mn == -INFINITY) continue;
-    const float f = expf(m - mn);
+    const float base = mn == -INFINITY ? 0.f : mn;  // (no maximum, but perhaps a NaN sum)
+    const float f = expf(m - base);
     den *= f;
     o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      if (ml[k].x == -INFINITY) continue;  // an empty partial's accumulator was never written
-      const float w = expf(ml[k].x - mn);
+      if (ml[k].y == 0.f) continue;  // an empty partial's accumulator was never written
+      const float w = expf(ml[k].x - base);
       den += w * ml[k].y;
       o = make_float4(fmaf(w, v[k].x, o.x), fmaf(w, v[k].y, o.y), fmaf(w, v[k].z, o.z), fmaf(w, v[k].w, o.w));
     }

@@ -45,7 +45,6 @@ constexpr int kPgItems = 2;                   // items described ahead
 constexpr int kPgItemCost = 8;                // units of an item beyond its tiles (see paged_tile_units)
 constexpr float kPgRescaleThreshold = 8.0f;   // log2 units
 constexpr int kPgSoftRegs = 208, kPgOtherRegs = 88;  // of the launch's 168 x 384 registers
-constexpr int kPgPolyPairs = 1;               // of 8 pairs, through the polynomial 2^x
 
 struct PagedTcParams {
   PagedAttnParams a;
@@ -760,13 +759,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             for (int e = 0; e < 32; ++e) {
               const float2 y = ffma2(make_float2(x[64 * h + 2 * e], x[64 * h + 2 * e + 1]), make_float2(c, c),
                                      make_float2(neg_m, neg_m));
-              float2 pe;
-              if ((e & 7) < kPgPolyPairs) {
-                pe = exp2_poly2(y);
-              } else {
-                pe.x = fast_exp2(y.x);
-                pe.y = fast_exp2(y.y);
-              }
+              // (the SFU keeps NaN; some pairs through a polynomial on the FMA pipe cost the same)
+              const float2 pe = make_float2(fast_exp2(y.x), fast_exp2(y.y));
               // P is rounded to bf16 for the MMA; the denominator sums the fp32 values
               w[e] = pack_bf16x2(pe.x, pe.y);
               if (e & 1)
@@ -931,8 +925,11 @@ __global__ void __launch_bounds__(kSplit ? 256 : 2 * D, kSplit ? 1 : 640 / D)
         const int64_t item = paged_item(prm, k == 0 ? b : -1, kvh, pi);
         // (all of these are on their way before the first is used; without a shared run the
         // shared items' cuts are stale, and not taken)
-        const int2 cut = prm.cuts[paged_item_of_all(prm, k == 0 ? b : -1, item)];
+        int2 cut = prm.cuts[paged_item_of_all(prm, k == 0 ? b : -1, item)];
         const int shared_runs = *prm.run_shared, L = prm.a.prefix_lens[b];
+        // (after a wait that gave up an entry may be missing: whatever it holds names CTAs)
+        cut.x = max(0, min(cut.x, prm.ctas - 1));
+        cut.y = max(0, min(cut.y, prm.ctas - 1));
         // (of a pair, the second row tile has the second slot)
         row0 = paged_part_row(prm, k == 0 ? b : -1, item, cut.x, nrow == 2 ? (rt & 1) : 0);
         step = 2 * (k == 0 ? prm.rows_own : prm.rows_sh);
@@ -977,14 +974,14 @@ __global__ void __launch_bounds__(kSplit ? 256 : 2 * D, kSplit ? 1 : 640 / D)
       float mn = m;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, ml[k].x);
-      if (mn == -INFINITY) continue;
-      const float f = exp2f(m - mn);
+      const float base = mn == -INFINITY ? 0.f : mn;  // (no maximum, but perhaps a NaN sum)
+      const float f = exp2f(m - base);
       den *= f;
       acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        if (ml[k].x == -INFINITY) continue;  // an empty partial's accumulator was never written
-        const float w = exp2f(ml[k].x - mn);
+        if (ml[k].y == 0.f) continue;  // an empty partial's accumulator was never written
+        const float w = exp2f(ml[k].x - base);
         den += w * ml[k].y;
         acc = make_float4(acc.x + w * v[k].x, acc.y + w * v[k].y, acc.z + w * v[k].z, acc.w + w * v[k].w);
       }
@@ -1000,11 +997,12 @@ __global__ void __launch_bounds__(kSplit ? 256 : 2 * D, kSplit ? 1 : 640 / D)
       float mn = -INFINITY;
 #pragma unroll
       for (int k = 0; k < 8; ++k) mn = fmaxf(mn, ml_s[k][lane].x);
+      if (mn == -INFINITY) mn = 0.f;
       den = 0.f;
       acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        if (ml_s[k][lane].x == -INFINITY) continue;
+        if (ml_s[k][lane].y == 0.f) continue;
         const float w = exp2f(ml_s[k][lane].x - mn);
         const float4 t = acc_s[k][lane];
         den += w * ml_s[k][lane].y;

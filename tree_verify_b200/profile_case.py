@@ -6,8 +6,10 @@ saves and restores device memory between its passes stays quick, and it prints n
 
 Stages: attention, lm_head, accept, step (eagle_verify_step), and the kernels around the step:
 commit (the root and accepted nodes of one walk into a cache with room for them), rerank
-(256 random candidates down to the workload's N nodes) and draft (the children of 10 draft
-nodes per sequence, k = 10, from logits over the workload's vocabulary).
+(256 random candidates down to the workload's N nodes), draft (the children of 10 draft
+nodes per sequence, k = 10, from logits over the workload's vocabulary), paged_attention (the
+workload's trees over a cache in pages of 64 positions, half of the prefix shared) and
+lm_head_scaled (the workload's LM head in e4m3, hidden rows quantised in the call).
 """
 from __future__ import annotations
 
@@ -30,7 +32,8 @@ def main() -> None:
     ap = argparse.ArgumentParser()
     ap.add_argument("--workload", default="vicuna7b_static", choices=sorted(wl.WORKLOADS))
     ap.add_argument("--stage", default="lm_head",
-                    choices=["attention", "lm_head", "accept", "step", "commit", "rerank", "draft"])
+                    choices=["attention", "lm_head", "accept", "step", "commit", "rerank", "draft",
+                             "paged_attention", "lm_head_scaled"])
     ap.add_argument("--temperature", type=float, default=1.0)
     ap.add_argument("--launches", type=int, default=3)
     args = ap.parse_args()
@@ -66,6 +69,49 @@ def main() -> None:
             torch.cuda.synchronize()
         assert binding.device_error(reset=True) == 0
         print(f"rerank x{args.launches} on {w.name}: ok")
+        return
+
+    if args.stage in ("paged_attention", "lm_head_scaled"):
+        dtype = torch.float32 if w.dtype == "fp32" else torch.bfloat16
+        gen = torch.Generator(device=dev).manual_seed(1234)
+
+        def normal(*shape):
+            return torch.randn(shape, generator=gen, device=dev).to(dtype)
+
+        if args.stage == "paged_attention":
+            page, D, Hkv, L = 64, w.head_dim, w.num_kv_heads, w.prefix_len
+            shared, width = L // 2, -(-L // page)
+            table = torch.arange(B * width, device=dev, dtype=torch.int32).view(B, width)
+            table[:, :shared // page] = table[0, :shared // page].clone()
+            lens = torch.full((B,), L, dtype=torch.int32, device=dev)
+            rng = np.random.default_rng(1234)
+            parents = torch.from_numpy(np.stack([wl.random_parents(rng, N, 10) for _ in range(B)])
+                                       .astype(np.int32)).to(dev)
+            q, k_tree, v_tree = normal(B, w.num_q_heads, N, D), normal(B, Hkv, N, D), normal(B, Hkv, N, D)
+            k_pages, v_pages = normal(B * width, Hkv, page, D), normal(B * width, Hkv, page, D)
+            out = torch.empty_like(q)
+            shape = shape_from_workload(w)
+            pages = binding.make_pages(B * width, page, width)
+            work = torch.empty(max(256, binding.paged_workspace_bytes(shape, pages, shared)), dtype=torch.uint8,
+                               device=dev)
+            calls = [lambda: binding.tree_attention_paged(shape, pages, q, k_pages, v_pages, table, lens, shared,
+                                                          k_tree, v_tree, parents, out, work)]
+        else:
+            M, H, V, e4m3 = B * N, w.hidden, w.vocab, torch.float8_e4m3fn
+            hidden, weight = normal(M, H), normal(V, H)
+            h8, w8 = torch.empty((M, H), dtype=e4m3, device=dev), torch.empty((V, H), dtype=e4m3, device=dev)
+            hs = torch.empty((-(-H // 128), -(-M // 4) * 4), dtype=torch.float32, device=dev)
+            ws = torch.empty((-(-V // 128), -(-H // 128)), dtype=torch.float32, device=dev)
+            logits = torch.empty((M, V), dtype=torch.float32, device=dev)
+            binding.quantize_blocks(weight, w8, ws)
+            calls = [lambda: binding.quantize_rows(hidden, h8, hs),
+                     lambda: binding.lm_head_logits_scaled(h8, hs, w8, ws, logits)]
+        for _ in range(args.launches):
+            for call in calls:
+                call()
+            torch.cuda.synchronize()
+        assert binding.device_error(reset=True) == 0
+        print(f"{args.stage} x{args.launches} on {w.name}: ok")
         return
 
     inp = wl.generate(w, args.temperature)
