@@ -65,7 +65,8 @@ def attention(q, k_pages, v_pages, table, lens, k_tree, v_tree, parents, scale, 
     Bound, per output element, with A = sum of w |v| over the row's keys:
       scores: a D-long fp32 sum is off by at most (D + 4) 2^-24 of sum |q k|, which moves a
         weight by that relative amount (es), in the numerator and in the denominator;
-      bf16 only: a weight is rounded to bf16 for its product with V (2^-8);
+      bf16 only: a weight is rounded to bf16 for its product with V (2^-8), and 2^x of some
+        weights comes from a polynomial within 1.1e-4, in numerator and denominator;
       exponents: x c - m in fp32 is off by 4 2^-24 |x c| (in es), ex2 itself by 2^-22;
       sums over n keys: n 2^-24 in each;
       one rounding of the result."""
@@ -90,7 +91,7 @@ def attention(q, k_pages, v_pages, table, lens, k_tree, v_tree, parents, scale, 
             es = ((d + 8) * EPS32 * mag * see[:, None]).amax(dim=-1, keepdim=True)
             rel = 2 * es + 2 * (2.0 ** -22 + (see.shape[1] + 64) * EPS32)
             if dtype == "bf16":
-                rel = rel + 2.0 ** -8
+                rel = rel + 2.0 ** -8 + 2 * 1.1e-4
             out[b, :, g * group:(g + 1) * group] = o
             bound[b, :, g * group:(g + 1) * group] = rel * a + HALF_STEP[dtype] * (o.abs() + rel * a)
     return out, bound

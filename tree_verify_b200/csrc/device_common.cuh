@@ -477,10 +477,17 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
 // error on [-1/2, 1/2] (1.0e-4, far below the bf16 rounding the result goes through); 2^j is
 // built directly in the exponent field.  y is clamped to >= -127, where that field is 0, so
 // -inf and everything below about -126.5 give exactly +0.  For y <= 128 only.
+// With kKeepNan a NaN stays one (the clamp otherwise takes it for -127).
+template <bool kKeepNan = false>
 __device__ __forceinline__ float2 exp2_poly2(float2 y) {
   constexpr float kShift = 12582912.0f;  // 1.5 * 2^23
-  y.x = fmaxf(y.x, -127.0f);
-  y.y = fmaxf(y.y, -127.0f);
+  if constexpr (kKeepNan) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(y.x) : "f"(-127.0f));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(y.y) : "f"(-127.0f));
+  } else {
+    y.x = fmaxf(y.x, -127.0f);
+    y.y = fmaxf(y.y, -127.0f);
+  }
   const float2 t = fadd2(y, make_float2(kShift, kShift));
   const float2 j = fadd2(t, make_float2(-kShift, -kShift));
   const float2 f = ffma2(j, make_float2(-1.0f, -1.0f), y);

@@ -44,6 +44,7 @@ constexpr int kHalf = kAttnKeys / 2;          // keys of half a tile; rows that 
 constexpr int kPgItems = 2;                   // items described ahead
 constexpr int kPgItemCost = 8;                // units of an item beyond its tiles (see paged_tile_units)
 constexpr float kPgRescaleThreshold = 8.0f;   // log2 units
+constexpr int kPgPolyPairs = 1;               // of 8 pairs, through the polynomial 2^x (2 % of pair tiles' time)
 constexpr int kPgSoftRegs = 208, kPgOtherRegs = 88;  // of the launch's 168 x 384 registers
 
 struct PagedTcParams {
@@ -759,8 +760,13 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             for (int e = 0; e < 32; ++e) {
               const float2 y = ffma2(make_float2(x[64 * h + 2 * e], x[64 * h + 2 * e + 1]), make_float2(c, c),
                                      make_float2(neg_m, neg_m));
-              // (the SFU keeps NaN; some pairs through a polynomial on the FMA pipe cost the same)
-              const float2 pe = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+              float2 pe;
+              if ((e & 7) < kPgPolyPairs) {
+                pe = exp2_poly2<true>(y);
+              } else {
+                pe.x = fast_exp2(y.x);
+                pe.y = fast_exp2(y.y);
+              }
               // P is rounded to bf16 for the MMA; the denominator sums the fp32 values
               w[e] = pack_bf16x2(pe.x, pe.y);
               if (e & 1)
