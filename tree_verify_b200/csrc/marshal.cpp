@@ -5,8 +5,9 @@
 //
 // Every function takes the arguments of its namesake in binding.py in order and returns the
 // library's status.  Tensors are dense device tensors of the current device (or None) of the
-// sizes and types that the shape says; the structures are the ctypes ones of binding.py.  The library is reached by the addresses
-// that bind() is given, so this module links to nothing of it.
+// sizes and types that the shape says; the structures are the ctypes ones of binding.py.  The
+// library is reached by the addresses that bind() is given, so this module links to nothing
+// of it.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

@@ -30,6 +30,12 @@
 //   warp 11          walks the CTA's items and hands their descriptions to the others
 // P of a tile lies over its S, so a group's next S is issued when its P V has completed.
 // P V of a tile's first 64 keys is issued while the softmax of the others runs.
+//
+// Measured, main kernel and merge: 64 nodes x 8 sequences, 32/8 heads of 128, 8192 shared and
+// 131..512 own keys: 84.5 us, 846 TFLOP/s; there the softmax chain of a tile (some 890
+// instructions a thread) bounds it, beside 2,048 of 3,750 clocks of MMAs.  60 nodes x 16
+// sequences of 32/32 heads over 500 + 12..3596 keys: 124 us, 4.1 TB/s, a tile's chain of loads,
+// MMAs and softmax.  One token over 4097 keys: 15 us, latency.
 #pragma once
 
 #include "attention.cuh"
@@ -895,7 +901,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 // of one row, kBatch partials at a time with all loads issued before any is used.  A warp is
 // 8 rows x 4 column groups: it reads 128-byte runs and writes whole sectors.  With kSplit,
 // for few rows, the CTA's 8 warps share one such group of columns and take every 8th partial
-// each.  The order of the sums does not depend on timing.
+// each.  The order of the sums does not depend on timing.  Latency-bound: 35 MB of partials
+// of 16384 rows take 14.9 us, a single token's 4.
 template <bool kSplit>
 constexpr int kPgMergeRows = kSplit ? 8 : 16;
 
