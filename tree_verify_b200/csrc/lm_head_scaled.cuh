@@ -72,7 +72,7 @@ __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, flo
 }
 
 // 1 x 128 blocks: one warp per block, four elements a lane.  Streaming, HBM- or
-// launch-bound: each element is read once (512 rows of 4096 in bf16: 6.8 us, 60 rows 3).
+// launch-bound: each element is read once (512 rows of 4096 in bf16: 6.8 us).
 template <typename T>
 __global__ void __launch_bounds__(128)
     quantize_rows_kernel(const T* __restrict__ x, uint8_t* __restrict__ x8, float* __restrict__ scales, int rows,
