@@ -253,7 +253,6 @@ eagle_status_t launch_paged_tc(const eagle_shape_t* s, const eagle_pages_t* pg, 
   p.rows_sh = plan.rows_sh;
   p.own_row0 = plan.own_row0;
   p.box = pg->page_size < kHalf ? pg->page_size : kHalf;
-  p.ctas = kNumSMs;
   p.scale_log2 = ap.scale * 1.4426950408889634f;
   CUtensorMap tq, tk, tv, tkt, tvt;
   using u64 = cuuint64_t;

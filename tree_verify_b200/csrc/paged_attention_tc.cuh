@@ -32,10 +32,10 @@
 // P V of a tile's first 64 keys is issued while the softmax of the others runs.
 //
 // Measured, main kernel and merge: 64 nodes x 8 sequences, 32/8 heads of 128, 8192 shared and
-// 131..512 own keys: 84.5 us, 846 TFLOP/s; there the softmax chain of a tile (some 890
+// 131..512 own keys: 83.5 us, 855 TFLOP/s; there the softmax chain of a tile (some 890
 // instructions a thread) bounds it, beside 2,048 of 3,750 clocks of MMAs.  60 nodes x 16
-// sequences of 32/32 heads over 500 + 12..3596 keys: 124 us, 4.1 TB/s, a tile's chain of loads,
-// MMAs and softmax.  One token over 4097 keys: 15 us, latency.
+// sequences of 32/32 heads over 500 + 12..3596 keys: 123 us, 4.2 TB/s, a tile's chain of loads,
+// MMAs and softmax.  One token over 4097 keys: 14.4 us, latency.
 #pragma once
 
 #include "attention.cuh"
@@ -65,7 +65,6 @@ struct PagedTcParams {
   int32_t rows_own, rows_sh;  // rows of a tile that can be real
   int64_t own_row0;           // first partial row of the own part
   int32_t box;          // rows of a TMA box: min(page size, 64)
-  int32_t ctas;         // pieces of the line of units
   float scale_log2;
 };
 
@@ -105,9 +104,11 @@ __device__ __forceinline__ int64_t paged_div(int64_t a, int64_t b) {
   return a / b;
 }
 // Pieces of a line of W units: no more than units, so that none is empty.
-__device__ __forceinline__ int paged_pieces(int64_t W, int ctas) { return W < ctas ? static_cast<int>(W) : ctas; }
-// Piece c is [c W / P, (c + 1) W / P).
-__device__ __forceinline__ int64_t paged_cut(int c, int64_t W, int P) { return paged_div(c * W, P); }
+__device__ __forceinline__ int paged_pieces(int64_t W) { return W < kNumSMs ? static_cast<int>(W) : kNumSMs; }
+// Piece c of P is [c W / P, (c + 1) W / P), of one unit each if W < kNumSMs.
+__device__ __forceinline__ int64_t paged_cut(int c, int64_t W) {
+  return W < kNumSMs ? c : static_cast<int64_t>(static_cast<uint64_t>(c * W) / kNumSMs);
+}
 
 // Walks the items of a piece [lo, hi) of the line.
 struct PagedCursor {
@@ -143,8 +144,9 @@ struct PagedCursor {
     const int64_t per = paged_head_units(T, rb);
     kvh = static_cast<int32_t>(paged_div(lo - base, per));
     const int64_t r = lo - base - kvh * per;
-    pi = static_cast<int32_t>(min(paged_div(r, 4 * static_cast<int64_t>(T) + kPgItemCost),
-                                  static_cast<int64_t>(((rb + 1) >> 1) - 1)));
+    pi = rb <= 2 ? 0
+                 : static_cast<int32_t>(min(paged_div(r, 4 * static_cast<int64_t>(T) + kPgItemCost),
+                                            static_cast<int64_t>(((rb + 1) >> 1) - 1)));
     u0 = base + kvh * per + paged_pair_units(T, pi);
   }
   __device__ __forceinline__ void next(const PagedTcParams& p) {
@@ -158,9 +160,15 @@ struct PagedCursor {
   }
   // the item's tiles [a, z) that start in [lo, hi)
   __device__ __forceinline__ void range(int64_t lo, int64_t hi, int& a, int& z) const {
-    const int w = paged_tile_units(nrow());
-    a = lo <= u0 ? 0 : static_cast<int>(min(paged_div(lo - u0 + w - 1, w), static_cast<int64_t>(T)));
-    z = hi <= u0 ? 0 : static_cast<int>(min(paged_div(hi - u0 + w - 1, w), static_cast<int64_t>(T)));
+    a = tiles_before(lo);
+    z = tiles_before(hi);
+  }
+  __device__ __forceinline__ int tiles_before(int64_t at) const {
+    if (at <= u0) return 0;
+    const bool pair = nrow() == 2;
+    if (at - u0 >= static_cast<int64_t>(pair ? 4 : 3) * T) return T;
+    const uint32_t u = static_cast<uint32_t>(at - u0);  // (T < 2^25)
+    return static_cast<int>(pair ? (u + 3) / 4 : (u + 2) / 3);
   }
 };
 
@@ -320,8 +328,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   const int64_t shared_units =
       run_shared ? Hkv * paged_head_units((prm.a.shared + kAttnKeys - 1) / kAttnKeys, prm.rb_sh) : 0;
   const int64_t W = shared_units + own_units;
-  const int P = paged_pieces(W, prm.ctas);
-  const int64_t lo = cta < P ? paged_cut(cta, W, P) : W, hi = cta < P ? paged_cut(cta + 1, W, P) : W;
+  const int P = paged_pieces(W);
+  const int64_t lo = cta < P ? paged_cut(cta, W) : W, hi = cta < P ? paged_cut(cta + 1, W) : W;
   start += shared_units;
   if (cta == 0 && tid == 0) *prm.run_shared = run_shared ? 1 : 0;
   {
@@ -914,7 +922,6 @@ __global__ void __launch_bounds__(kSplit ? 256 : 2 * D, kSplit ? 1 : 640 / D)
   __shared__ int32_t count_s[2][kRows], step_s[2][kRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();  // (a next call's main kernel sets itself up meanwhile)
-  pdl_wait();
   if (threadIdx.x < 2 * kRows) {
     // thread = (own or shared runs, row): the first partial's row, the step to the next,
     // their number
@@ -936,13 +943,14 @@ __global__ void __launch_bounds__(kSplit ? 256 : 2 * D, kSplit ? 1 : 640 / D)
       if (rb > 0) {
         const int rt = nd / static_cast<uint32_t>(prm.NB), pi = rt >> 1, nrow = min(2, rb - 2 * pi);
         const int64_t item = paged_item(prm, k == 0 ? b : -1, kvh, pi);
-        // (all of these are on their way before the first is used; without a shared run the
-        // shared items' cuts are stale, and not taken)
+        // (nothing before this is the main kernel's; all of these are on their way before the
+        // first is used; without a shared run the shared items' cuts are stale, and not taken)
+        pdl_wait();
         int2 cut = prm.cuts[paged_item_of_all(prm, k == 0 ? b : -1, item)];
         const int shared_runs = *prm.run_shared, L = prm.a.prefix_lens[b];
         // (after a wait that gave up an entry may be missing: whatever it holds names CTAs)
-        cut.x = max(0, min(cut.x, prm.ctas - 1));
-        cut.y = max(0, min(cut.y, prm.ctas - 1));
+        cut.x = max(0, min(cut.x, kNumSMs - 1));
+        cut.y = max(0, min(cut.y, kNumSMs - 1));
         // (of a pair, the second row tile has the second slot)
         row0 = paged_part_row(prm, k == 0 ? b : -1, item, cut.x, nrow == 2 ? (rt & 1) : 0);
         step = 2 * (k == 0 ? prm.rows_own : prm.rows_sh);
@@ -956,6 +964,7 @@ __global__ void __launch_bounds__(kSplit ? 256 : 2 * D, kSplit ? 1 : 640 / D)
     row0_s[k][j] = row0;
     if (k == 0) out_s[j] = orow;
   }
+  pdl_wait();
   __syncthreads();
   const int col = (kSplit ? blockIdx.y : warp) * 4 + (lane >> 3);  // group of four columns
   const int first = kSplit ? warp : 0, stride = kSplit ? 8 : 1;
