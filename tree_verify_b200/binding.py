@@ -139,8 +139,12 @@ def workspace_bytes(shape: Shape) -> int:
 # ---------------------------------------------------------------- tensor marshalling
 
 def _ptr(t) -> Optional[int]:
-    if t is None or type(t) is int:
+    if t is None:
+        return None
+    if isinstance(t, int):
         return t
+    import torch
+    assert isinstance(t, torch.Tensor)
     if not t.is_cuda:
         raise ValueError("library arguments are device tensors")
     if not t.is_contiguous():
@@ -148,22 +152,11 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-_current_stream = None
-
-
 def _stream(stream) -> Optional[int]:
-    global _current_stream
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    if _current_stream is None:
-        import torch
-        torch.cuda.current_stream()  # (initialises CUDA)
-        raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
-        if raw is not None and device is not None:  # the same handle without a Stream object around it
-            _current_stream = lambda: raw(device())
-        else:
-            _current_stream = lambda: torch.cuda.current_stream().cuda_stream
-    return _current_stream()
+    import torch
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check(fn: str, code: int) -> None:
