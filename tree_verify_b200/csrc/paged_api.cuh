@@ -72,14 +72,18 @@ bool allow_smem(int bytes) {
 // Kernels whose first warps take `inc` registers a thread out of what the CTA was launched
 // with, the last four keeping `dec`: a build that was launched with fewer would wait for
 // ever, so it is never launched.
-template <typename K>
-bool register_shares_fit(K kernel, int threads, int inc, int dec) {
+template <auto kKernel>
+bool register_shares_fit(int threads, int inc, int dec) {
+  static std::atomic<bool> fit{false};  // (the same on every device; asked again after an error)
+  if (fit.load(std::memory_order_relaxed)) return true;
   cudaFuncAttributes a{};
-  if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess) {
+  if (cudaFuncGetAttributes(&a, kKernel) != cudaSuccess) {
     cudaGetLastError();
     return false;
   }
-  return a.numRegs * threads >= (threads - 128) * inc + 128 * dec;
+  if (a.numRegs * threads < (threads - 128) * inc + 128 * dec) return false;
+  fit.store(true, std::memory_order_relaxed);
+  return true;
 }
 
 // ------------------------------------------------------------------ append
@@ -235,8 +239,9 @@ template <int D>
 eagle_status_t launch_paged_tc(const eagle_shape_t* s, const eagle_pages_t* pg, const PagedAttnParams& ap,
                                const void* q, const void* kp, const void* vp, const void* kt, const void* vt,
                                void* out, void* ws, cudaStream_t st) {
-  static const bool shares = register_shares_fit(paged_attn_tc_kernel<D>, kPgThreads, kPgSoftRegs, kPgOtherRegs);
-  if (!shares || !allow_smem<paged_attn_tc_kernel<D>>(PgSmem<D>::kAlloc)) return EAGLE_ERR_CUDA;
+  if (!register_shares_fit<paged_attn_tc_kernel<D>>(kPgThreads, kPgSoftRegs, kPgOtherRegs) ||
+      !allow_smem<paged_attn_tc_kernel<D>>(PgSmem<D>::kAlloc))
+    return EAGLE_ERR_CUDA;
   const PagedPlan plan = plan_paged(s, ap.shared);
   PagedTcParams p{};
   p.a = ap;
@@ -605,9 +610,8 @@ eagle_status_t eagle_lm_head_logits_scaled(int32_t rows, int32_t hidden, int32_t
   const int64_t tiles = static_cast<int64_t>(prm.stages) * row_tiles;
   const unsigned grid = static_cast<unsigned>(tiles < kNumSMs ? tiles : kNumSMs);
   if (nv == 2) {
-    static const bool shares =
-        register_shares_fit(lm_head_scaled_rows_kernel<2, 128>, kScRowsThreads, kScRowsEpiRegs, kScRowsOtherRegs);
-    if (!shares) return EAGLE_ERR_CUDA;
+    if (!register_shares_fit<lm_head_scaled_rows_kernel<2, 128>>(kScRowsThreads, kScRowsEpiRegs, kScRowsOtherRegs))
+      return EAGLE_ERR_CUDA;
     return launch_scaled<lm_head_scaled_rows_kernel<2, 128>>(tw, th, prm, grid, kScRowsThreads,
                                                              ScaledRowsCfg<2, 128>::kAlloc, st);
   }
