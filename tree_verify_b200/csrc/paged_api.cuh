@@ -300,8 +300,7 @@ eagle_status_t launch_paged_tc(const eagle_shape_t* s, const eagle_pages_t* pg, 
   // CTAs per SM
   const int64_t rows = static_cast<int64_t>(ap.B) * ap.N * ap.Hq;
   const bool split = (rows + 7) / 8 * (D / 16) <= 4 * kNumSMs;
-  const int per = split ? kPgMergeRows<true> : kPgMergeRows<false>;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + per - 1) / per), split ? D / 16 : 1);
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kPgMergeRows - 1) / kPgMergeRows), split ? D / 16 : 1);
   cfg.blockDim = dim3(split ? 256 : 2 * D);
   cfg.dynamicSmemBytes = 0;
   const cudaError_t e = split ? cudaLaunchKernelEx(&cfg, paged_attn_merge_kernel<D, true>, p)

@@ -32,10 +32,10 @@
 // P V of a tile's first 64 keys is issued while the softmax of the others runs.
 //
 // Measured, main kernel and merge: 64 nodes x 8 sequences, 32/8 heads of 128, 8192 shared and
-// 131..512 own keys: 83.5 us, 855 TFLOP/s; there the softmax chain of a tile (some 890
+// 131..512 own keys: 82 us, 870 TFLOP/s; there the softmax chain of a tile (some 890
 // instructions a thread) bounds it, beside 2,048 of 3,750 clocks of MMAs.  60 nodes x 16
 // sequences of 32/32 heads over 500 + 12..3596 keys: 123 us, 4.2 TB/s, a tile's chain of loads,
-// MMAs and softmax.  One token over 4097 keys: 14.4 us, latency.
+// MMAs and softmax.  One token over 4097 keys: 14.3 us, latency.
 #pragma once
 
 #include "attention.cuh"
@@ -905,19 +905,18 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 
 // ------------------------------------------------------------------ merge
 // Output row = the sum of its partials weighted by 2^(m_p - m), over the sum of their l.
-// A CTA takes kRows rows, neighbours in the partials, eight at a time; a thread four columns
-// of one row, kBatch partials at a time with all loads issued before any is used.  A warp is
-// 8 rows x 4 column groups: it reads 128-byte runs and writes whole sectors.  With kSplit,
-// for few rows, the CTA's 8 warps share one such group of columns and take every 8th partial
-// each.  The order of the sums does not depend on timing.  Latency-bound: 35 MB of partials
-// of 16384 rows take 14.9 us, a single token's 4.
-template <bool kSplit>
-constexpr int kPgMergeRows = kSplit ? 8 : 16;
+// A CTA takes 8 rows, neighbours in the partials; a thread four columns of one row, kBatch
+// partials at a time with all loads issued before any is used.  A warp is 8 rows x 4 column
+// groups: it reads 128-byte runs and writes whole sectors.  With kSplit, for few rows, the
+// CTA's 8 warps share one such group of columns and take every 8th partial each.  The order of
+// the sums does not depend on timing.  Latency-bound: 35 MB of partials of 16384 rows take 9 us
+// from L2, a single token's 2.6 (16 rows a CTA: 10.5; 2, 3 or 8 partials at a time: 9 to 30).
+constexpr int kPgMergeRows = 8;
 
 template <int D, bool kSplit>
 __global__ void __launch_bounds__(kSplit ? 256 : 2 * D, kSplit ? 1 : 640 / D)
     paged_attn_merge_kernel(const __grid_constant__ PagedTcParams prm) {
-  constexpr int kBatch = 4, kRows = kPgMergeRows<kSplit>;
+  constexpr int kBatch = 4, kRows = kPgMergeRows;
   __shared__ int64_t row0_s[2][kRows], out_s[kRows];
   __shared__ int32_t count_s[2][kRows], step_s[2][kRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -968,74 +967,72 @@ __global__ void __launch_bounds__(kSplit ? 256 : 2 * D, kSplit ? 1 : 640 / D)
   __syncthreads();
   const int col = (kSplit ? blockIdx.y : warp) * 4 + (lane >> 3);  // group of four columns
   const int first = kSplit ? warp : 0, stride = kSplit ? 8 : 1;
-#pragma unroll 1
-  for (int j = lane & 7; j < kRows; j += 8) {
-    const int n0 = count_s[0][j], total = n0 + count_s[1][j];
-    if (!kSplit && total <= 1) continue;  // the run that holds the whole item wrote the output (0: no row)
-    const int64_t base0 = row0_s[0][j] >> 7, base1 = row0_s[1][j] >> 7;
-    const int r0 = static_cast<int>(row0_s[0][j] & 127), r1 = static_cast<int>(row0_s[1][j] & 127);
-    const int st0 = step_s[0][j], st1 = step_s[1][j];
-    float m = -INFINITY, den = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = first; i0 < total; i0 += kBatch * stride) {
-      float2 ml[kBatch];
-      float4 v[kBatch];
+  const int j = lane & 7;
+  const int n0 = count_s[0][j], total = n0 + count_s[1][j];
+  if (!kSplit && total <= 1) return;  // the run that holds the whole item wrote the output (0: no row)
+  const int64_t base0 = row0_s[0][j] >> 7, base1 = row0_s[1][j] >> 7;
+  const int r0 = static_cast<int>(row0_s[0][j] & 127), r1 = static_cast<int>(row0_s[1][j] & 127);
+  const int st0 = step_s[0][j], st1 = step_s[1][j];
+  float m = -INFINITY, den = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = first; i0 < total; i0 += kBatch * stride) {
+    float2 ml[kBatch];
+    float4 v[kBatch];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int i = i0 + k * stride;
-        ml[k] = make_float2(-INFINITY, 0.f);
-        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < total) {
-          const bool own = i < n0;
-          const int64_t base = own ? base0 + static_cast<int64_t>(i) * st0 : base1 + static_cast<int64_t>(i - n0) * st1;
-          const int r = own ? r0 : r1, rows = own ? prm.rows_own : prm.rows_sh;
-          ml[k] = prm.part_ml[base + r];
-          v[k] = *(reinterpret_cast<const float4*>(prm.part_acc + base * D) + static_cast<size_t>(col) * rows + r);
-        }
-      }
-      float mn = m;
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, ml[k].x);
-      const float base = mn == -INFINITY ? 0.f : mn;  // (no maximum, but perhaps a NaN sum)
-      const float f = exp2f(m - base);
-      den *= f;
-      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        if (ml[k].y == 0.f) continue;  // an empty partial's accumulator was never written
-        const float w = exp2f(ml[k].x - base);
-        den += w * ml[k].y;
-        acc = make_float4(acc.x + w * v[k].x, acc.y + w * v[k].y, acc.z + w * v[k].z, acc.w + w * v[k].w);
-      }
-      m = mn;
-    }
-    if constexpr (kSplit) {
-      __shared__ float4 acc_s[8][32];
-      __shared__ float2 ml_s[8][32];
-      acc_s[warp][lane] = acc;
-      ml_s[warp][lane] = make_float2(m, den);
-      __syncthreads();
-      if (warp != 0) return;
-      float mn = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) mn = fmaxf(mn, ml_s[k][lane].x);
-      if (mn == -INFINITY) mn = 0.f;
-      den = 0.f;
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (ml_s[k][lane].y == 0.f) continue;
-        const float w = exp2f(ml_s[k][lane].x - mn);
-        const float4 t = acc_s[k][lane];
-        den += w * ml_s[k][lane].y;
-        acc = make_float4(acc.x + w * t.x, acc.y + w * t.y, acc.z + w * t.z, acc.w + w * t.w);
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * stride;
+      ml[k] = make_float2(-INFINITY, 0.f);
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < total) {
+        const bool own = i < n0;
+        const int64_t base = own ? base0 + static_cast<int64_t>(i) * st0 : base1 + static_cast<int64_t>(i - n0) * st1;
+        const int r = own ? r0 : r1, rows = own ? prm.rows_own : prm.rows_sh;
+        ml[k] = prm.part_ml[base + r];
+        v[k] = *(reinterpret_cast<const float4*>(prm.part_acc + base * D) + static_cast<size_t>(col) * rows + r);
       }
     }
-    if (total <= 1) continue;
-    const float inv = 1.0f / den;  // the node itself is always visible
-    *reinterpret_cast<uint2*>(prm.out + out_s[j] * D + col * 4) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    float mn = m;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, ml[k].x);
+    const float base = mn == -INFINITY ? 0.f : mn;  // (no maximum, but perhaps a NaN sum)
+    const float f = exp2f(m - base);
+    den *= f;
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (ml[k].y == 0.f) continue;  // an empty partial's accumulator was never written
+      const float w = exp2f(ml[k].x - base);
+      den += w * ml[k].y;
+      acc = make_float4(acc.x + w * v[k].x, acc.y + w * v[k].y, acc.z + w * v[k].z, acc.w + w * v[k].w);
+    }
+    m = mn;
   }
+  if constexpr (kSplit) {
+    __shared__ float4 acc_s[8][32];
+    __shared__ float2 ml_s[8][32];
+    acc_s[warp][lane] = acc;
+    ml_s[warp][lane] = make_float2(m, den);
+    __syncthreads();
+    if (warp != 0) return;
+    float mn = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mn = fmaxf(mn, ml_s[k][lane].x);
+    if (mn == -INFINITY) mn = 0.f;
+    den = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (ml_s[k][lane].y == 0.f) continue;
+      const float w = exp2f(ml_s[k][lane].x - mn);
+      const float4 t = acc_s[k][lane];
+      den += w * ml_s[k][lane].y;
+      acc = make_float4(acc.x + w * t.x, acc.y + w * t.y, acc.z + w * t.z, acc.w + w * t.w);
+    }
+  }
+  if (total <= 1) return;
+  const float inv = 1.0f / den;  // the node itself is always visible
+  *reinterpret_cast<uint2*>(prm.out + out_s[j] * D + col * 4) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
 }  // namespace eagle
