@@ -72,7 +72,7 @@ def main() -> None:
         return
 
     if args.stage in ("paged_attention", "lm_head_scaled"):
-        dtype = torch.float32 if w.dtype == "fp32" else torch.bfloat16
+        dtype = torch.bfloat16 if w.dtype == wl.BF16 else torch.float32
         gen = torch.Generator(device=dev).manual_seed(1234)
 
         def normal(*shape):
