@@ -1,6 +1,8 @@
 """The paged-cache and e4m3 entry points reject bad arguments with a status before any CUDA
 call (nothing here launches work)."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -242,3 +244,39 @@ def test_plain_attention_sees_prefix_and_ancestors_only():
     vals = torch.cat([vp[2, 0], vp[0, 0, :1], vt[0, [0, 2], 0]]).double()
     want = torch.softmax(keys @ q[0, 2, 0].double() * 0.125, 0) @ vals
     assert torch.allclose(out[0, 2, 0], want, atol=1e-12)
+
+
+# ------------------------------------------------------------------ waits that give up
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "tree_verify_b200", "csrc")
+
+
+def _kernel_body(name, kernel):
+    """The kernel's body, without comments."""
+    with open(os.path.join(CSRC, name)) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    at = text.index("{", text.index(kernel + "("))
+    depth = 0
+    for i in range(at, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[at:i], text
+    raise AssertionError(f"{kernel} has no end")
+
+
+@pytest.mark.parametrize("name,kernel", [("paged_attention_tc.cuh", "paged_attn_tc_kernel"),
+                                         ("lm_head_scaled.cuh", "lm_head_scaled_kernel"),
+                                         ("lm_head_scaled.cuh", "lm_head_scaled_rows_kernel")])
+def test_a_warp_that_gave_up_leaves_nobody_at_a_barrier(name, kernel):
+    """A warp whose bounded wait runs out leaves its loop alone and goes to the end of the kernel.
+    Barriers that wait without a limit may so only stand where every thread passes once,
+    outside all branches and loops; between warps of one role there are only bounded waits."""
+    body, text = _kernel_body(name, kernel)
+    assert not re.search(r"\bbar(rier)?(\.cta)?\.(sync|arrive|red)", text)
+    depth, found = 0, 0
+    for token in re.findall(r"[{}]|__syncthreads\w*\(|\bmbar_wait\(", body):
+        depth += {"{": 1, "}": -1}.get(token, 0)
+        if token.startswith("__syncthreads"):
+            found += 1
+            assert depth == 1, f"a block barrier at depth {depth}"
+    assert found >= 2

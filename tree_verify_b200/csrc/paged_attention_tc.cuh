@@ -216,8 +216,8 @@ struct PgSmem {
   static constexpr int kBarOff = kFirstOff + 16;
   // q_full[2], k_full, k_empty, v_full, v_empty, s_full[2], p_half[2], p_full[2], pv_done[2],
   // turn[2], all_done[2],
-  // item_full, item_empty
-  static constexpr int kNumBars = 2 + 2 * kKStages + 2 * kVStages + 12 + 2 * kPgItems;
+  // item_full, item_empty, met
+  static constexpr int kNumBars = 2 + 2 * kKStages + 2 * kVStages + 12 + 2 * kPgItems + 1;
   static constexpr int kBytes = kBarOff + kNumBars * 8 + 16;
   static constexpr int kAlloc = kBytes + 1024;
   static constexpr uint32_t kTmemCols = 512;
@@ -225,9 +225,6 @@ struct PgSmem {
   static_assert(kAlloc <= 227 * 1024, "shared memory");
   static_assert(kXchOff % 8 == 0 && kBarOff % 8 == 0, "alignment");
 };
-
-// Both softmax groups.
-__device__ __forceinline__ void both_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 template <int D>
 __global__ void __launch_bounds__(kPgThreads, 1)
@@ -253,6 +250,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   const uint32_t s_full = v_empty + 8 * SV, p_half = s_full + 16, p_full = p_half + 16;
   const uint32_t pv_done = p_full + 16, turn = pv_done + 16, all_done = turn + 16;
   const uint32_t item_full = all_done + 16, item_empty = item_full + 8 * kPgItems;
+  const uint32_t met = item_empty + 8 * kPgItems;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kBarOff + SM::kNumBars * 8);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -282,6 +280,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       mbar_init(item_full + 8 * s, 1);
       mbar_init(item_empty + 8 * s, kPgReaders);
     }
+    mbar_init(met, 8);  // one arrival per warp of both groups
     fence_mbar_init();
   }
   if (warp == kPgMmaWarp) {
@@ -642,6 +641,16 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     auto wait = [&](uint32_t bar, uint32_t parity) {
       if (ok) ok = mbar_wait(bar, parity, kErrAttnConsumerWait);
     };
+    // Both groups meet.  A warp whose waits have given up leaves the items on its own, so this
+    // is a bounded wait like all others, not a barrier of the hardware's: the rest give up too.
+    uint32_t meets = 0;
+    auto meet_groups = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(met);
+      wait(met, meets++ & 1);
+      tc_fence_after();
+    };
     for (int i = 0;; ++i) {
       ok = __all_sync(0xffffffffu, ok && run_wait(i, kErrAttnConsumerWait));
       if (!ok) break;
@@ -840,8 +849,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         // the sums meet here: both O are in this warp's TMEM lanes, and each group brings half
         // of the columns out
         if (g == 1) xch[r] = make_float2(m_ref, l);
-        tc_fence_before();
-        both_sync();
+        meet_groups();
         if (g == 0) {
           const float2 x = xch[r];
           const float m = fmaxf(m_ref, x.x);
@@ -855,8 +863,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
           }
           xch[r] = make_float2(w1, w0);
         }
-        both_sync();
-        tc_fence_after();
+        meet_groups();
         if (g == 1) {
           w0 = xch[r].x;
           w1 = xch[r].y;
@@ -887,10 +894,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       // (an empty run's partial says so)
       if (rvalid && !direct && (nrow == 2 || (meet || z == a ? g == 0 : any)))
         prm.part_ml[prow + r] = make_float2(m_ref, l);
-      if (meet) {  // neither group lets its next P V at its O before the other has read it
-        tc_fence_before();
-        both_sync();
-      }
+      if (meet) meet_groups();  // neither group lets its next P V at its O before the other has read it
       base += z - a;
     }
   }
