@@ -152,6 +152,16 @@ def test_append_bad_arguments(lib):
     assert _append(lib, ko=FAKE + 9 * (1 << 22)) == INVALID        # keys over the rotated queries
 
 
+def test_append_in_place_spares_only_the_operand_itself(lib):
+    """An input that lies where the in-place operand does is read while that one is rotated."""
+    q, k, v, kp, vp, qo = (FAKE + i * (1 << 22) for i in (0, 1, 2, 6, 7, 9))
+    alone = dict(num_q_heads=2, num_kv_heads=2)
+    assert _append(lib, v=k, ko=k) == INVALID                      # values = keys, keys in place
+    assert _append(lib, s=_shape(**alone), k=q, qo=q) == INVALID   # keys = queries, queries in place
+    assert _append(lib, s=_shape(**alone), v=q, qo=q) == INVALID   # values = queries
+    assert _append(lib, k=q, ko=q, qo=qo) == INVALID               # queries over the keys, keys in place
+
+
 # ------------------------------------------------------------------ commit
 
 def _commit(lib, s=None, pg=None, ptrs=None):

@@ -112,13 +112,14 @@ struct RowSpan {
   }
 };
 
-// A rotated output (dense) either is its own dense input or lies apart from every input.
-bool rotated_out_ok(const void* out, int64_t width, const RowSpan& own, const RowSpan (&in)[3], int64_t rows,
-                    int esize) {
-  if (out == own.p && own.stride != width) return false;
-  for (const RowSpan& x : in) {
-    if (x.p == nullptr || (x.p == own.p && out == own.p)) continue;
-    if (overlap(x.p, x.bytes(rows, esize), out, static_cast<size_t>(rows * width * esize))) return false;
+// A rotated output (dense) either is its own dense input, in[own], or lies apart from every
+// input; in place too it lies apart from the others, wherever they begin.
+bool rotated_out_ok(const void* out, int64_t width, int own, const RowSpan (&in)[3], int64_t rows, int esize) {
+  const bool in_place = out == in[own].p;
+  if (in_place && in[own].stride != width) return false;
+  for (int i = 0; i < 3; ++i) {
+    if (in[i].p == nullptr || (i == own && in_place)) continue;
+    if (overlap(in[i].p, in[i].bytes(rows, esize), out, static_cast<size_t>(rows * width * esize))) return false;
   }
   return true;
 }
@@ -384,9 +385,9 @@ eagle_status_t eagle_rope_append(const eagle_shape_t* shape, const eagle_pages_t
       (seq_ids != nullptr && (k == nullptr || v == nullptr || !rows_ok(v, v_stride, kw, esize, n))))
     return EAGLE_ERR_INVALID_ARGUMENT;
   const RowSpan in[3] = {{q, q_stride, qw}, {k, k_stride, kw}, {seq_ids != nullptr ? v : nullptr, v_stride, kw}};
-  if (q != nullptr && !rotated_out_ok(q_out, qw, in[0], in, n, esize)) return EAGLE_ERR_INVALID_ARGUMENT;
+  if (q != nullptr && !rotated_out_ok(q_out, qw, 0, in, n, esize)) return EAGLE_ERR_INVALID_ARGUMENT;
   if (k_out != nullptr &&
-      (k == nullptr || !aligned16(k_out) || !rotated_out_ok(k_out, kw, in[1], in, n, esize) ||
+      (k == nullptr || !aligned16(k_out) || !rotated_out_ok(k_out, kw, 1, in, n, esize) ||
        (q != nullptr && overlap(q_out, static_cast<size_t>(n * qw * esize), k_out,
                                 static_cast<size_t>(n * kw * esize)))))
     return EAGLE_ERR_INVALID_ARGUMENT;
