@@ -386,7 +386,8 @@ typedef struct {
  *     then their sines (unused with rotary_dim = 0).
  *   q_out [R, Hq, D] dtype; k_out [R, Hkv, D] dtype or NULL: the rotated keys as a dense array
  *     (the k_tree of a draft tree).  Either may be its own input if that is dense; otherwise
- *     an output overlaps no input and not the other output.
+ *     an output overlaps no input, not the other output and not the pages.
+ *   No input row lies over a slot that the call writes for another row.
  * A row whose position lies outside the table or the cache, or whose sequence is outside
  * [-1, B), is skipped whole and records device error 0x401 (0x206 for its page index).
  * R = num_rows >= 0.  Uses shape's batch, heads, head_dim and dtype.  No workspace.

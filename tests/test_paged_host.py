@@ -162,6 +162,16 @@ def test_append_in_place_spares_only_the_operand_itself(lib):
     assert _append(lib, k=q, ko=q, qo=qo) == INVALID               # queries over the keys, keys in place
 
 
+@pytest.mark.parametrize("rows", [1, 7])
+def test_append_outputs_apart_from_the_cache(lib, rows):
+    s, pool = _shape(), 64 * 2 * 16 * 128 * 2                      # bytes of the default pools
+    kp, vp = FAKE + 6 * (1 << 22), FAKE + 7 * (1 << 22)
+    for name, heads in (("qo", 8), ("ko", 2)):
+        for base in (kp, vp):
+            for at in (0, pool - 16, 16 - rows * heads * 128 * 2):
+                assert _append(lib, s=s, rows=rows, **{name: base + at}) == INVALID, (name, at)
+
+
 # ------------------------------------------------------------------ commit
 
 def _commit(lib, s=None, pg=None, ptrs=None):

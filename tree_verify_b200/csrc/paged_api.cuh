@@ -49,6 +49,11 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   return x < y + bn && y < x + an;
 }
 
+// Bytes of a page pool.
+size_t pool_bytes(const eagle_pages_t* pg, const eagle_shape_t* s, int esize) {
+  return static_cast<size_t>(pg->num_pages) * pg->page_size * s->num_kv_heads * s->head_dim * esize;
+}
+
 int elem_size(const eagle_shape_t* s) { return s->dtype == EAGLE_DTYPE_BF16 ? 2 : 4; }
 
 // ------------------------------------------------------------------ kernel attributes
@@ -396,6 +401,12 @@ eagle_status_t eagle_rope_append(const eagle_shape_t* shape, const eagle_pages_t
     rc = check_pages(pages);
     if (rc != EAGLE_OK) return rc;
     if (!aligned16(k_pages) || !aligned16(v_pages) || page_table == nullptr) return EAGLE_ERR_INVALID_ARGUMENT;
+    const size_t pool = pool_bytes(pages, shape, esize);
+    for (const void* cache : {k_pages, v_pages}) {
+      if ((q != nullptr && overlap(q_out, static_cast<size_t>(n * qw * esize), cache, pool)) ||
+          (k_out != nullptr && overlap(k_out, static_cast<size_t>(n * kw * esize), cache, pool)))
+        return EAGLE_ERR_INVALID_ARGUMENT;
+    }
     p.map = page_map(pages, page_table);
   } else if (k != nullptr && k_out == nullptr) {
     return EAGLE_ERR_INVALID_ARGUMENT;  // keys that go nowhere
