@@ -104,6 +104,18 @@ def test_attention_overlaps_and_longest_cache(lib):
     assert binding.paged_workspace_bytes(_shape(max_prefix_len=(1 << 31) - 512), _pages(**wide), 0) == 0
 
 
+@pytest.mark.parametrize("dtype,esize", [("bf16", 2), ("f32", 4)])
+def test_attention_out_apart_from_the_cache_and_the_indices(lib, dtype, esize):
+    out_bytes = 2 * 13 * 8 * 128 * esize
+    # k_pages, v_pages, page_table, prefix_lens, parents of the default sizes
+    for i, n in ((1, 64 * 2 * 16 * 128 * esize), (2, 64 * 2 * 16 * 128 * esize), (3, 2 * 32 * 4), (4, 2 * 4),
+                 (7, 2 * 13 * 4)):
+        for at in (0, (n - 1) // 16 * 16, 16 - out_bytes):
+            p = [FAKE + (j << 22) for j in range(9)]
+            p[8] = p[i] + at
+            assert _attend(lib, s=_shape(dtype=dtype), ptrs=p, ws=FAKE + (9 << 22)) == INVALID, (i, at)
+
+
 # ------------------------------------------------------------------ append
 
 def _append(lib, s=None, pg=None, rope=(600, 64, 0), rows=7, **kw):

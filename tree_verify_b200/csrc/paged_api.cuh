@@ -457,10 +457,15 @@ eagle_status_t eagle_tree_attention_paged(const eagle_shape_t* shape, const eagl
                               workspace_bytes, eagle_paged_workspace_bytes(shape, pages, shared_len));
   if (rc != EAGLE_OK) return rc;
   if (page_table == nullptr) return EAGLE_ERR_INVALID_ARGUMENT;
-  // queries and tree are read by some CTAs while others write outputs
-  const size_t row = static_cast<size_t>(shape->batch) * shape->num_nodes * shape->head_dim * elem_size(shape);
-  const size_t qn = row * shape->num_q_heads, tn = row * shape->num_kv_heads;
-  if (overlap(out, qn, q, qn) || overlap(out, qn, k_tree, tn) || overlap(out, qn, v_tree, tn))
+  // inputs are read by some CTAs while others write outputs
+  const int esize = elem_size(shape);
+  const size_t nodes = static_cast<size_t>(shape->batch) * shape->num_nodes, row = nodes * shape->head_dim * esize;
+  const size_t qn = row * shape->num_q_heads, tn = row * shape->num_kv_heads, pool = pool_bytes(pages, shape, esize);
+  const size_t table = static_cast<size_t>(shape->batch) * pages->max_pages * sizeof(int32_t);
+  if (overlap(out, qn, q, qn) || overlap(out, qn, k_tree, tn) || overlap(out, qn, v_tree, tn) ||
+      overlap(out, qn, k_pages, pool) || overlap(out, qn, v_pages, pool) || overlap(out, qn, page_table, table) ||
+      overlap(out, qn, prefix_lens, shape->batch * sizeof(int32_t)) ||
+      overlap(out, qn, parents, nodes * sizeof(int32_t)))
     return EAGLE_ERR_INVALID_ARGUMENT;
   PagedAttnParams p{};
   p.map = page_map(pages, page_table);
