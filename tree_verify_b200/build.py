@@ -63,10 +63,10 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    # the library first: C programs need it where the module's compiler or headers are missing
+    if force or _stale(LIB, SOURCES + HEADERS):
+        _compile([NVCC, *NVCC_FLAGS, *SOURCES], LIB, verbose)
     build_marshal(force, verbose)
-    if not force and not _stale(LIB, SOURCES + HEADERS):
-        return LIB
-    _compile([NVCC, *NVCC_FLAGS, *SOURCES], LIB, verbose)
     return LIB
 
 
