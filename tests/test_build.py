@@ -27,3 +27,11 @@ def test_the_library_is_built_where_the_module_cannot_be(monkeypatch, tmp_path, 
     with pytest.raises(RuntimeError):
         b.build(force=force)
     assert [name for name, _ in made] == ["libeagle_verify.so", "_marshal.so"]
+
+
+def test_the_compiler_is_looked_up_at_the_call(monkeypatch, tmp_path):
+    made = _fake_compiler(monkeypatch, tmp_path)
+    monkeypatch.setenv("NVCC", "/opt/other/bin/nvcc")
+    with pytest.raises(RuntimeError):
+        b.build()
+    assert made[0] == ("libeagle_verify.so", "/opt/other/bin/nvcc")

@@ -17,13 +17,16 @@ SOURCES = [os.path.join(CSRC, "eagle_verify.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
     os.path.join(ROOT, "include", "eagle_verify.h")]
 
-NVCC = os.environ.get("NVCC", "nvcc")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
     "-Xcompiler", "-fPIC", "-shared",
     "-Xptxas", "-v",
 ]
+
+
+def _nvcc() -> str:
+    return os.environ.get("NVCC", "nvcc")
 
 
 def _stale(target: str, sources) -> bool:
@@ -51,7 +54,7 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
 
     import torch
     base = os.path.dirname(torch.__file__)
-    cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(NVCC) or "/usr/local/cuda/bin/nvcc")))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(_nvcc()) or "/usr/local/cuda/bin/nvcc")))
     lib = os.path.join(base, "lib")
     _compile([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
@@ -65,7 +68,7 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
 def build(force: bool = False, verbose: bool = False) -> str:
     # the library first: C programs need it where the module's compiler or headers are missing
     if force or _stale(LIB, SOURCES + HEADERS):
-        _compile([NVCC, *NVCC_FLAGS, *SOURCES], LIB, verbose)
+        _compile([_nvcc(), *NVCC_FLAGS, *SOURCES], LIB, verbose)
     build_marshal(force, verbose)
     return LIB
 
