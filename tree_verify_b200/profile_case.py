@@ -87,7 +87,7 @@ def main() -> None:
             rng = np.random.default_rng(1234)
             parents = torch.from_numpy(np.stack([wl.random_parents(rng, N, 10) for _ in range(B)])
                                        .astype(np.int32)).to(dev)
-            q, k_tree, v_tree = normal(B, w.num_q_heads, N, D), normal(B, Hkv, N, D), normal(B, Hkv, N, D)
+            q, k_tree, v_tree = normal(B, N, w.num_q_heads, D), normal(B, N, Hkv, D), normal(B, N, Hkv, D)
             k_pages, v_pages = normal(B * width, Hkv, page, D), normal(B * width, Hkv, page, D)
             out = torch.empty_like(q)
             shape = shape_from_workload(w)
