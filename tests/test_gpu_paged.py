@@ -656,6 +656,54 @@ def test_tensors_that_do_not_fit_are_refused(cuda_lib):
             cuda_lib.lm_head_logits_scaled(*bad)
 
 
+def test_tensors_in_another_order_are_refused(cuda_lib):
+    """Dense tensors of the right size whose dimensions are swapped; merged or split dimensions
+    are the same memory and are taken."""
+    B, N, Hq, Hkv, D, H = 2, 3, 4, 2, 64, 64
+    c = _case(16, B, N, Hq, Hkv, D, 16, 0, [40, 20], "bf16")
+    d = {k: v.cuda() for k, v in c.items() if isinstance(v, torch.Tensor)}
+    shape = cuda_lib.make_shape(B, N, Hq, Hkv, D, 40, H, 128, "bf16")
+    num = d["k_pages"].shape[0]
+    pages = cuda_lib.make_pages(num, 16, d["table"].shape[1])
+    ws = torch.empty(cuda_lib.paged_workspace_bytes(shape, pages, 0), dtype=torch.uint8, device="cuda")
+    args = dict(q=d["q"], k_pages=d["k_pages"], v_pages=d["v_pages"], page_table=d["table"], prefix_lens=d["lens"],
+                shared_len=0, k_tree=d["k_tree"], v_tree=d["v_tree"], parents=d["parents"],
+                out=torch.empty_like(d["q"]), workspace=ws)
+    call = lambda **kw: cuda_lib.tree_attention_paged(shape, pages, **{**args, **kw})
+    swap = lambda t: t.transpose(-3, -2).contiguous() if t.dim() > 2 else t.t().contiguous()
+    call()
+    for name in ("q", "k_tree", "v_tree", "k_pages", "v_pages", "out", "page_table", "parents"):
+        other = swap(args[name])
+        for bad in (other, other.flatten(0, 1)) if other.dim() == 4 else (other,):
+            with pytest.raises(ValueError):
+                call(**{name: bad})
+    for q, kt, kp in ((d["q"].view(B * N, Hq, D), d["k_tree"].view(B, N, -1), d["k_pages"].view(num * Hkv, 16, D)),
+                      (d["q"].view(B, N, Hkv, Hq // Hkv, D), d["k_tree"].view(-1), d["k_pages"].view(num, Hkv, -1)),
+                      (d["q"].view(B * N, Hkv, Hq // Hkv, D), d["k_tree"][None], d["k_pages"].view(1, num, Hkv, 16, 1, D))):
+        out = torch.empty_like(q)
+        call(q=q, k_tree=kt, k_pages=kp, out=out)
+        assert torch.equal(out.view(-1), args["out"].view(-1))
+    # append: the rotated keys as [heads, R, D]
+    k, pos = torch.zeros((5, Hkv, D), dtype=torch.bfloat16, device="cuda"), torch.zeros((5,), dtype=torch.int32, device="cuda")
+    cs = torch.zeros((40, D), device="cuda")
+    rope = lambda k_out: cuda_lib.rope_append(shape, None, None, k, None, pos, None, cs, None, None, None, None, k_out)
+    rope(torch.empty_like(k).view(5, -1))
+    with pytest.raises(ValueError):
+        rope(torch.empty((Hkv, 5, D), dtype=torch.bfloat16, device="cuda"))
+    # commit: hidden rows and features as [N, B, H], paths as [N, B]
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    rows = torch.zeros((B * N, H), dtype=torch.bfloat16, device="cuda")
+    commit = lambda hidden, acc, feat: cuda_lib.commit_accepted_paged(
+        shape, pages, d["k_pages"], d["v_pages"], d["table"], i32(B), d["k_tree"], d["v_tree"], hidden, d["parents"], acc,
+        torch.full((B,), -1, dtype=torch.int32, device="cuda"), i32(B), feat)
+    commit(rows, i32(B, N), torch.zeros_like(rows).view(B, N, H))
+    commit(rows.view(B, N, H), i32(B * N), torch.zeros_like(rows))
+    for bad in ((rows.view(N, B, H), i32(B, N), torch.zeros_like(rows)), (rows, i32(N, B), torch.zeros_like(rows)),
+                (rows, i32(B, N), torch.zeros_like(rows).view(N, B, H))):
+        with pytest.raises(ValueError):
+            commit(*bad)
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

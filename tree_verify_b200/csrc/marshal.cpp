@@ -5,9 +5,9 @@
 //
 // Every function takes the arguments of its namesake in binding.py in order and returns the
 // library's status.  Tensors are dense device tensors of the current device (or None) of the
-// sizes and types that the shape says; the structures are the ctypes ones of binding.py.  The
-// library is reached by the addresses that bind() is given, so this module links to nothing
-// of it.
+// types and dimensions that the shape says (neighbouring dimensions may be merged or split);
+// the structures are the ctypes ones of binding.py.  The library is reached by the addresses
+// that bind() is given, so this module links to nothing of it.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -16,6 +16,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
+#include <initializer_list>
 
 #include "../../include/eagle_verify.h"
 
@@ -46,22 +47,61 @@ const at::Tensor& tensor(PyObject* o) {
   return t;
 }
 
-// A dense tensor's memory, if it has that many elements of that type; None is a null pointer.
+using Dims = std::initializer_list<int64_t>;
+
+// Whether a dense tensor of as many elements (at least one) holds them in the order of an
+// array `want`: its dimensions are those, some neighbours of either side merged into one.  With
+// dimensions swapped ([B, heads, N, D] for [B, N, heads, D]) both sides have a boundary inside
+// a stretch that has no common one.
+bool same_order(const at::Tensor& t, Dims want) {
+  // products of the last dimensions, from 1 to the number of elements
+  int64_t i = t.dim(), have = 1, need = 1;
+  const int64_t* w = want.end();
+  bool inner_have = false, inner_need = false;
+  auto next_have = [&] {
+    const int64_t before = have;
+    while (i > 0 && have == before) have *= t.size(--i);
+  };
+  auto next_need = [&] {
+    const int64_t before = need;
+    while (w != want.begin() && need == before) need *= *--w;
+  };
+  for (const int64_t numel = t.numel(); have != numel || need != numel;) {
+    if (have == need) {
+      inner_have = inner_need = false;
+      next_have();
+      next_need();
+    } else if (have < need) {
+      inner_have = true;
+      next_have();
+    } else {
+      inner_need = true;
+      next_need();
+    }
+    if (inner_have && inner_need) return false;
+  }
+  return true;
+}
+
+// A dense tensor's memory, if it is that array of that type; None is a null pointer.
 template <typename T = void>
-T* ptr(PyObject* o, int64_t numel, at::ScalarType type) {
+T* ptr(PyObject* o, Dims dims, at::ScalarType type) {
   if (o == Py_None) return nullptr;
   const at::Tensor& t = tensor(o);
   if (!t.is_contiguous()) throw BadArgument("library arguments are contiguous tensors");
+  int64_t numel = 1;
+  for (const int64_t d : dims) numel *= d;
   if (t.numel() != numel || t.scalar_type() != type)
     throw BadArgument("a tensor does not have the size or the type that the shape says");
+  if (numel > 0 && !same_order(t, dims)) throw BadArgument("a tensor does not have the dimensions that the shape says");
   return static_cast<T*>(t.data_ptr());
 }
-int32_t* ints(PyObject* o, int64_t numel) { return ptr<int32_t>(o, numel, at::kInt); }
-float* floats(PyObject* o, int64_t numel) { return ptr<float>(o, numel, at::kFloat); }
+int32_t* ints(PyObject* o, Dims dims) { return ptr<int32_t>(o, dims, at::kInt); }
+float* floats(PyObject* o, Dims dims) { return ptr<float>(o, dims, at::kFloat); }
 // e4m3 values, or their bytes
-void* bytes(PyObject* o, int64_t numel) {
+void* bytes(PyObject* o, Dims dims) {
   const bool raw = THPVariable_Check(o) && THPVariable_Unpack(o).scalar_type() == at::kByte;
-  return ptr(o, numel, raw ? at::kByte : at::kFloat8_e4m3fn);
+  return ptr(o, dims, raw ? at::kByte : at::kFloat8_e4m3fn);
 }
 
 // [R, heads, D] whose rows may be strided parts of a wider array.
@@ -129,7 +169,7 @@ int32_t integer(PyObject* o) {
 // What the shape says of the cache.  Its numbers are the library's to refuse; here they only
 // size tensors.
 struct Sizes {
-  int64_t B, N, Hq, Hkv, D, H, pool, table;
+  int64_t B, N, Hq, Hkv, D, H, pages, page_size, max_pages;
   at::ScalarType type;
   Sizes(const eagle_shape_t* s, const eagle_pages_t* pg) {
     if (s == nullptr) throw BadArgument("a shape is expected");
@@ -139,10 +179,14 @@ struct Sizes {
     Hkv = s->num_kv_heads;
     D = s->head_dim;
     H = s->hidden;
-    pool = pg == nullptr ? 0 : static_cast<int64_t>(pg->num_pages) * pg->page_size * Hkv * D;
-    table = pg == nullptr ? 0 : B * pg->max_pages;
+    pages = pg == nullptr ? 0 : pg->num_pages;
+    page_size = pg == nullptr ? 0 : pg->page_size;
+    max_pages = pg == nullptr ? 0 : pg->max_pages;
     type = s->dtype == EAGLE_DTYPE_BF16 ? at::kBFloat16 : at::kFloat;
   }
+  void* pool(PyObject* o) const { return ptr(o, {pages, Hkv, page_size, D}, type); }
+  int32_t* table(PyObject* o) const { return ints(o, {B, max_pages}); }
+  void* nodes(PyObject* o, int64_t heads) const { return ptr(o, {B, N, heads, D}, type); }
 };
 
 int32_t dtype(const at::Tensor& t) {
@@ -220,10 +264,9 @@ PyObject* rope_append(PyObject*, Args a, Py_ssize_t n) {
       rope.interleaved = truth;
     }
     return g_entry.rope_append(
-        shape.p, pages.p, &rope, static_cast<int32_t>(R), q.p, q.stride, k.p, k.stride, v.p, v.stride, ints(a[5], R),
-        ints(a[6], R), floats(a[7], static_cast<int64_t>(rope.table_len) * rope.rotary_dim), ptr(a[8], z.pool, z.type),
-        ptr(a[9], z.pool, z.type), ints(a[10], z.table), ptr(a[11], R * z.Hq * z.D, z.type),
-        ptr(a[12], R * z.Hkv * z.D, z.type), stream(a[14]));
+        shape.p, pages.p, &rope, static_cast<int32_t>(R), q.p, q.stride, k.p, k.stride, v.p, v.stride, ints(a[5], {R}),
+        ints(a[6], {R}), floats(a[7], {rope.table_len, rope.rotary_dim}), z.pool(a[8]), z.pool(a[9]), z.table(a[10]),
+        ptr(a[11], {R, z.Hq, z.D}, z.type), ptr(a[12], {R, z.Hkv, z.D}, z.type), stream(a[14]));
   });
 }
 
@@ -234,14 +277,12 @@ PyObject* tree_attention_paged(PyObject*, Args a, Py_ssize_t n) {
     const Struct<eagle_shape_t> shape(a[0]);
     const Struct<eagle_pages_t> pages(a[1]);
     const Sizes z(shape.p, pages.p);
-    const int64_t q = z.B * z.N * z.Hq * z.D, kv = z.B * z.N * z.Hkv * z.D;
     int64_t space = 0;
     if (a[12] != Py_None) space = tensor(a[12]).numel();
     return g_entry.tree_attention_paged(
-        shape.p, pages.p, ptr(a[2], q, z.type), ptr(a[3], z.pool, z.type), ptr(a[4], z.pool, z.type),
-        ints(a[5], z.table), ints(a[6], z.B), integer(a[7]), ptr(a[8], kv, z.type), ptr(a[9], kv, z.type),
-        ints(a[10], z.B * z.N), ptr(a[11], q, z.type), ptr(a[12], space, at::kByte), static_cast<size_t>(space),
-        stream(a[13]));
+        shape.p, pages.p, z.nodes(a[2], z.Hq), z.pool(a[3]), z.pool(a[4]), z.table(a[5]), ints(a[6], {z.B}),
+        integer(a[7]), z.nodes(a[8], z.Hkv), z.nodes(a[9], z.Hkv), ints(a[10], {z.B, z.N}), z.nodes(a[11], z.Hq),
+        ptr(a[12], {space}, at::kByte), static_cast<size_t>(space), stream(a[13]));
   });
 }
 
@@ -252,11 +293,10 @@ PyObject* commit_accepted_paged(PyObject*, Args a, Py_ssize_t n) {
     const Struct<eagle_shape_t> shape(a[0]);
     const Struct<eagle_pages_t> pages(a[1]);
     const Sizes z(shape.p, pages.p);
-    const int64_t kv = z.B * z.N * z.Hkv * z.D, rows = z.B * z.N;
     return g_entry.commit_accepted_paged(
-        shape.p, pages.p, ptr(a[2], z.pool, z.type), ptr(a[3], z.pool, z.type), ints(a[4], z.table), ints(a[5], z.B),
-        ptr(a[6], kv, z.type), ptr(a[7], kv, z.type), ptr(a[8], rows * z.H, z.type), ints(a[9], rows),
-        ints(a[10], rows), ints(a[11], z.B), ints(a[12], z.B), ptr(a[13], rows * z.H, z.type), stream(a[14]));
+        shape.p, pages.p, z.pool(a[2]), z.pool(a[3]), z.table(a[4]), ints(a[5], {z.B}), z.nodes(a[6], z.Hkv),
+        z.nodes(a[7], z.Hkv), ptr(a[8], {z.B, z.N, z.H}, z.type), ints(a[9], {z.B, z.N}), ints(a[10], {z.B, z.N}),
+        ints(a[11], {z.B}), ints(a[12], {z.B}), ptr(a[13], {z.B, z.N, z.H}, z.type), stream(a[14]));
   });
 }
 
@@ -278,8 +318,8 @@ PyObject* quantize_rows(PyObject*, Args a, Py_ssize_t n) {
     if (!is(a[1], R, H) || !is(a[2], (H + 127) / 128, (R + 3) / 4 * 4))
       throw BadArgument("x_out is [R, H] and scales [ceil(H / 128), R rounded up to 4]");
     return g_entry.quantize_rows(static_cast<int32_t>(R), static_cast<int32_t>(H), dtype(x),
-                                 ptr(a[0], R * H, x.scalar_type()), bytes(a[1], R * H),
-                                 floats(a[2], (H + 127) / 128 * ((R + 3) / 4 * 4)), stream(a[3]));
+                                 ptr(a[0], {R, H}, x.scalar_type()), bytes(a[1], {R, H}),
+                                 floats(a[2], {(H + 127) / 128, (R + 3) / 4 * 4}), stream(a[3]));
   });
 }
 
@@ -292,8 +332,8 @@ PyObject* quantize_blocks(PyObject*, Args a, Py_ssize_t n) {
     if (!is(a[1], V, H) || !is(a[2], (V + 127) / 128, (H + 127) / 128))
       throw BadArgument("w_out is [V, H] and scales [ceil(V / 128), ceil(H / 128)]");
     return g_entry.quantize_blocks(static_cast<int32_t>(V), static_cast<int32_t>(H), dtype(w),
-                                   ptr(a[0], V * H, w.scalar_type()), bytes(a[1], V * H),
-                                   floats(a[2], (V + 127) / 128 * ((H + 127) / 128)), stream(a[3]));
+                                   ptr(a[0], {V, H}, w.scalar_type()), bytes(a[1], {V, H}),
+                                   floats(a[2], {(V + 127) / 128, (H + 127) / 128}), stream(a[3]));
   });
 }
 
@@ -310,8 +350,8 @@ PyObject* lm_head_logits_scaled(PyObject*, Args a, Py_ssize_t n) {
           "operands are x [R, H], x_scales [KB, R rounded up to 4], w [V, H], "
           "w_scales [ceil(V / 128), KB] and logits [R, V]");
     return g_entry.lm_head_logits_scaled(static_cast<int32_t>(R), static_cast<int32_t>(H), static_cast<int32_t>(V),
-                                         bytes(a[0], R * H), floats(a[1], KB * ((R + 3) / 4 * 4)), bytes(a[2], V * H),
-                                         floats(a[3], (V + 127) / 128 * KB), floats(a[4], R * V), stream(a[5]));
+                                         bytes(a[0], {R, H}), floats(a[1], {KB, (R + 3) / 4 * 4}), bytes(a[2], {V, H}),
+                                         floats(a[3], {(V + 127) / 128, KB}), floats(a[4], {R, V}), stream(a[5]));
   });
 }
 
