@@ -151,3 +151,78 @@ def test_quantize_then_logits_in_a_graph_and_on_a_stream(cuda_lib, rows):
         q, s = ref.quantize(host, 1)
         want, bound = ref.logits_scaled(q, s.t(), w8.cpu(), ws.cpu())
         assert ((logits.double().cpu() - want).abs() <= bound).all()
+
+
+# ------------------------------------------------------------------ tiles of two vocabulary blocks
+
+# 888 (pair of vocabulary blocks, row tile) pairs and more, which is where these tiles begin:
+# odd numbers of blocks, vocabularies that are no multiple of 4 (or of the last block's rows),
+# one to four row tiles, more K blocks than the ring has slots and fewer
+WIDE = [(129, 640, 113701), (300, 272, 75780), (65, 160, 227301), (385, 1040, 56577), (512, 528, 57000)]
+
+
+def _wide_reference(ops):
+    """As ref.logits_scaled, on the device: the largest take a CPU minutes."""
+    return ref.logits_scaled(*[t.cuda() for t in ops])
+
+
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("rows,hidden,vocab", WIDE)
+def test_scaled_logits_two_blocks(cuda_lib, rows, hidden, vocab, offset):
+    blocks = -(-vocab // 128)
+    assert (blocks + 1) // 2 * -(-rows // 128) >= 6 * 148
+    ops = _operands(rows + vocab, rows, hidden, vocab)
+    full = torch.full((rows * vocab + 64,), float("nan"), device="cuda")
+    logits = full[offset:offset + rows * vocab].view(rows, vocab)
+    d = [t.cuda() for t in ops]
+    cuda_lib.lm_head_logits_scaled(*d, logits)
+    torch.cuda.synchronize()
+    assert torch.isnan(full[:offset]).all() and torch.isnan(full[offset + rows * vocab:]).all()
+    want, bound = _wide_reference(ops)
+    got = logits.double()
+    assert torch.isfinite(got).all()
+    assert ((got - want).abs() <= bound).all(), ((got - want).abs() / bound.clamp(min=1e-300)).max()
+    again = torch.empty_like(logits)
+    cuda_lib.lm_head_logits_scaled(*d, again)
+    assert torch.equal(again, logits)
+
+
+def test_scaled_logits_two_blocks_keep_rows_apart(cuda_lib):
+    """A row whose scale is NaN is NaN as a whole, a vocabulary block whose scale is NaN in every
+    row; all else is as without them."""
+    rows, hidden, vocab = WIDE[0]
+    x8, xs, w8, ws = [t.cuda() for t in _operands(4, rows, hidden, vocab)]
+    clean, logits = torch.empty((rows, vocab), device="cuda"), torch.empty((rows, vocab), device="cuda")
+    cuda_lib.lm_head_logits_scaled(x8, xs, w8, ws, clean)
+    xs[2, 100] = xs[4, 128] = ws[888, 0] = ws[301, 3] = float("nan")   # block 888 is the last, alone in its tile
+    cuda_lib.lm_head_logits_scaled(x8, xs, w8, ws, logits)
+    hit = torch.zeros((rows, vocab), dtype=torch.bool, device="cuda")
+    hit[[100, 128]] = True
+    hit[:, 888 * 128:] = hit[:, 301 * 128:302 * 128] = True
+    assert torch.isfinite(clean).all() and torch.equal(torch.isnan(logits), hit)
+    assert torch.equal(logits[~hit], clean[~hit])
+
+
+# ------------------------------------------------------------------ whole outputs
+
+@pytest.mark.parametrize("rows,hidden,vocab", SIZES + WIDE[:2])
+def test_scaled_logits_whole_output(cuda_lib, rows, hidden, vocab):
+    """The errors of a whole output, as a root of squares, against its terms'.
+
+    The bound of a single logit counts every rounding at its worst and grows with H; together
+    they are random and add as squares.  A block's 128 exact products are summed in four steps
+    of 32, each losing at most 2^-23 of a partial sum whose root mean square is the block's at
+    most, and its scaling and addition round once each (2^-24, of the sum so far): per block
+    sqrt(4) 2^-23 of its own size, and over KB blocks, whose sums grow as the root of their
+    number, sqrt(2 KB / 2) 2^-24 of the whole.  For KB <= 32 that is below 2^-21 + 2^-21.4, and
+    2^-20 is the limit."""
+    ops = _operands(rows * 3 + vocab, rows, hidden, vocab)
+    assert -(-hidden // 128) <= 32
+    logits = torch.empty((rows, vocab), device="cuda")
+    x8, xs, w8, ws = [t.cuda() for t in ops]
+    cuda_lib.lm_head_logits_scaled(x8, xs, w8, ws, logits)
+    want, _ = _wide_reference(ops)
+    x = x8.float().double() * xs[:, :rows].double().t().repeat_interleave(128, 1)[:, :hidden]
+    w = w8.float().double() * ws.double().repeat_interleave(128, 0)[:vocab].repeat_interleave(128, 1)[:, :hidden]
+    size = ((x * x) @ (w * w).t()).sum().sqrt()   # the root of the terms' squares
+    assert (logits.double() - want).norm() <= 2.0 ** -20 * size
