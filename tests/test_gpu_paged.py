@@ -142,6 +142,55 @@ def test_attention(cuda_lib, case, dtype):
     _check(c, out)
 
 
+PLAN = [
+    # more than 384 sequences, two and three to a thread of the plan: some or none shorter than
+    # the shared prefix, empty ones, none that holds it
+    (400, 1, 2, 1, 64, 16, 0, [(i * 17) % 41 for i in range(400)]),
+    (769, 1, 4, 2, 64, 16, 20, [(i * 17) % 61 for i in range(769)]),
+    (800, 2, 4, 1, 128, 16, 33, [33 + (i * 31) % 300 for i in range(800)]),
+    (385, 1, 2, 1, 128, 32, 50, [(i * 13) % 50 for i in range(385)]),
+    # three row tiles of a sequence and 43 of the batch: pairs and single tiles in turn on a CTA
+    (17, 40, 64, 8, 64, 64, 200, [200 + 300 + (i * 397) % 1000 for i in range(17)]),
+    (6, 41, 16, 2, 128, 16, 300, [300 + (i * 397) % 1000 for i in range(6)]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("case", PLAN, ids=lambda c: f"B{c[0]}N{c[1]}H{c[2]}_{c[3]}D{c[4]}p{c[5]}s{c[6]}L{max(c[7])}")
+def test_attention_large_batches_and_odd_row_tiles(cuda_lib, case, dtype):
+    c = _case(len(case[7]) * 1000 + case[1], *case, dtype)
+    _, out, call, guards = _launcher(cuda_lib, c)
+    call()
+    guards()
+    _check(c, out)
+    first = out.clone()
+    for _ in range(3):
+        out.fill_(7.0)
+        call()
+        assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("case", ATTN + PLAN, ids=lambda c: f"B{c[0]}N{c[1]}H{c[2]}_{c[3]}D{c[4]}p{c[5]}s{c[6]}L{max(c[7])}")
+def test_attention_f32_whole_output(cuda_lib, case):
+    """The errors of a whole fp32 output, as a root of squares, against the output's.
+
+    A score's D-long chain of multiply-adds has partial sums that grow as the root of their
+    number: together they lose sqrt(D / 2) 2^-24 of a score of about 1.  The scaled score, its
+    difference from the maximum (magnitudes up to about 4) and the exponential round by at most
+    6 2^-24 more, the n-long sum over the keys by sqrt(n / 2) 2^-24; the rescalings of the
+    running sums and the merge belong to that count.  Twice their sum is the limit."""
+    c = _case(len(case[7]) * 77 + case[1], *case, "f32")
+    _, out, call, guards = _launcher(cuda_lib, c)
+    call()
+    guards()
+    B, N, Hq, D = c["q"].shape
+    want, _ = ref.attention(c["q"], c["k_pages"], c["v_pages"], c["table"], c["lens"], c["k_tree"], c["v_tree"],
+                            c["parents"], D ** -0.5, "f32")
+    n = max(case[7]) + N
+    limit = 2 * 2.0 ** -24 * ((D / 2) ** 0.5 + 6 + (n / 2) ** 0.5)
+    assert (out.double().cpu() - want).norm() <= limit * want.norm()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_copied_prefix_large_values_and_scale(cuda_lib, dtype):
     """Copies of the shared pages; scores spread so widely that rows rest on a few keys and
