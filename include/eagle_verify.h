@@ -419,7 +419,8 @@ eagle_status_t eagle_rope_append(const eagle_shape_t *shape, const eagle_pages_t
  * nodes that a node does not see.  Values are not masked but weighted by 0: an infinity or a
  * NaN in a node's v_tree reaches every node of its tree.  A needed position on a page outside
  * [0, num_pages) counts as a zero key and value.
- * max_prefix_len <= max_pages * page_size and < 2^31 - 512.  out overlaps no input.  Calls that may overlap need workspaces of their
+ * max_prefix_len <= max_pages * page_size and < 2^31 - 512.  out overlaps no input, the page
+ * pools and the index arrays among them.  Calls that may overlap need workspaces of their
  * own, graphs that may run at the same time too.
  */
 size_t eagle_paged_workspace_bytes(const eagle_shape_t *shape, const eagle_pages_t *pages,
@@ -458,8 +459,8 @@ eagle_status_t eagle_commit_accepted_paged(const eagle_shape_t *shape, const eag
  *   w_scales  [ceil(V / 128), KB] fp32
  *   logits    [R, V] fp32
  * Any fp32 scales are taken whose products x_scales * w_scales, which are formed first, are
- * finite.  No output overlaps an input or another output.  eagle_quantize_rows / eagle_quantize_blocks make them from dtype
- * (eagle_dtype_t) values: per block the power of two 2^e with the smallest e >= -126 for which
+ * finite.  No output overlaps an input or another output.
+ * eagle_quantize_rows / eagle_quantize_blocks make them from dtype (eagle_dtype_t) values: per block the power of two 2^e with the smallest e >= -126 for which
  * the block's largest magnitude is <= 448 * 2^e, elements rounded to nearest even after an
  * exact division by it.  A block that holds an infinity or a NaN gets a NaN scale.  R = 0 is
  * allowed and does nothing.  No workspace.

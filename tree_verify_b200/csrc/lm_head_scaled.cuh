@@ -7,12 +7,13 @@
 // them in fp32 (measured against fp64: relative error 1.3e-8 on normal data, as an fp32 FMA
 // chain); the blocks are scaled and summed in fp32 registers.
 //
-// Two forms, by the number of tree rows (each measured at both sizes, see the kernels):
+// Two forms, by the number of tree rows (times of the product alone, without the quantiser):
 //   up to 16 rows    swap-AB like lm_head.cuh: 128 vocabulary rows are the MMA's M, the tree
-//                    rows its N; the weight streams once and bounds it (a row of
-//                    32000 x 4096: 22 us, 6.0 TB/s, the other form 32; 32 rows: 27 and 25);
+//                    rows its N; the weight streams once and bounds it (32000 x 4096: 1 row
+//                    23.0 us, 5.7 TB/s, the other form 30.6; 16 rows 24.6 and 28.0).  A thread
+//                    has 8 accumulators: 16 rows are all that it takes;
 //   more             tree rows as M (128 a tile), one or two blocks of 128 vocabulary rows
-//                    as N, so that a thread's accumulators all share one scale.
+//                    as N, so that a thread's accumulators all share one scale (32 rows 24.6).
 // In both, per K block one 128-deep MMA chain goes into a fresh TMEM buffer and eight
 // epilogue warps scale it into their register accumulators while the next blocks' MMAs run.
 #pragma once
@@ -71,8 +72,10 @@ __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, flo
   f[3] = __uint_as_float(w.y & 0xFFFF0000u);
 }
 
-// 1 x 128 blocks: one warp per block, four elements a lane.  Streaming, HBM- or
-// launch-bound: each element is read once (512 rows of 4096 in bf16: 6.8 us).
+// 1 x 128 blocks: one warp per block, four elements a lane.  Each element is read once.
+// Latency-bound: a thread has one load in flight, then the block's maximum, then its store.
+// 512 rows of 4096 in bf16: 5.1 us, 1.2 TB/s (6.8 from a cold cache, at 8 % of HBM); one row
+// 1.4 us.
 template <typename T>
 __global__ void __launch_bounds__(128)
     quantize_rows_kernel(const T* __restrict__ x, uint8_t* __restrict__ x8, float* __restrict__ scales, int rows,
@@ -96,7 +99,8 @@ __global__ void __launch_bounds__(128)
 }
 
 // 128 x 128 blocks: one CTA per block, a warp per 16 of its rows, the block kept in
-// registers between its maximum and its rounding.  HBM-bound; run when a weight is loaded.
+// registers between its maximum and its rounding.  Run when a weight is loaded.  128256 x 4096:
+// fp32 378 us, 6.9 TB/s, HBM-bound; bf16 321 us, 4.9 TB/s, with loads of 8 bytes a lane.
 template <typename T>
 __global__ void __launch_bounds__(256)
     quantize_blocks_kernel(const T* __restrict__ w, uint8_t* __restrict__ w8, float* __restrict__ scales, int rows,
@@ -337,11 +341,11 @@ __global__ void __launch_bounds__(kScThreads, 2)
 // block and two vocabulary blocks TMA writes 48 KB and the MMAs read 48 KB in 512 MMA
 // clocks.  The logits leave through a 2 KB patch per warp, so that whole sectors are written
 // (each thread writing its own row instead: 360 us against 318 on 512 rows of 128256 x 4096).
-// That case runs at about 1,050 clocks per K block under the power cap, 307 us at 1.6 GHz and
-// up to 350 on warmer cards: 160 are the stores, 590 the MMAs and their operands alone, the
+// That case runs at about 1,050 clocks per K block under the power cap, 296 to 304 us at first
+// and 344 once the card is warm: 160 are the stores, 590 the MMAs and their operands alone, the
 // rest the hand-offs of the two TMEM buffers.  Sixteen epilogue warps with a quarter of the
 // columns each took the same time, swap-AB with 256 tree rows as N 747.  60 rows of 32000 x
-// 8192: 51 us, 5.3 TB/s, HBM-bound.
+// 8192: 46 us, 5.8 TB/s, HBM-bound.
 
 // Warps 0-7 epilogue, 8 TMA, 9 MMA; 10 and 11 only complete a group of four, which is what
 // registers are moved between.

@@ -49,7 +49,7 @@ __device__ __forceinline__ size_t page_row(const PageMap& m, int32_t page, int g
 // Pure streaming: every element is read once and written once.  One CTA per row, so the
 // row's cosines come from L1 after the first head; a thread takes two 16-byte chunks at a
 // time (for halves the two that hold the pairs), all loads before the stores.  8,191 rows of
-// 32/8 heads of 128 in bf16: 35 us, 5.9 TB/s, HBM-bound; 8 rows: 2.7 us, of which an empty
+// 32/8 heads of 128 in bf16: 35 us, 5.8 TB/s, HBM-bound; 8 rows: 2.8 us, of which an empty
 // launch is 2.2.
 
 struct AppendParams {
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(const Appen
 // commit_kernel (commit.cuh) with the cache rows found through the page table: the same
 // checks of the path, plus every page the new rows land on, before anything is written.
 // Latency-bound: path, page and copy follow one another.  One walk of a 45-node tree, 32 kv
-// heads of 128: 3.2 us; 64 walks of 60-node trees, 8 kv heads, hidden 8192: 5.1 us.
+// heads of 128: 2.8 us; 64 walks of 60-node trees, 8 kv heads, hidden 8192: 4.4 us.
 
 struct CommitPagedParams {
   uint8_t* k_pages;

@@ -132,9 +132,10 @@ bool rotated_out_ok(const void* out, int64_t width, int own, const RowSpan (&in)
 // ------------------------------------------------------------------ attention
 
 // The fp32 form's row tiles: 4 or 16 rows where no more are in a sequence's kv head (32 tokens
-// of 32/8 heads over 1000 + 0..3000 keys: 4 rows 264 us, 16 rows 372); else 64, or 32 where 64
-// would leave most SMs with a tile or two (three 13-node trees over 333 + 0..300 keys: 32 rows
-// 16.0 us, 64 rows 18.5; eight 64-node trees over 1000 + 0..500: 581 and 492).  Key tiles are
+// of 32/8 heads over 1000 shared + 0..3000 keys: 4 rows 261 us, 16 rows 391); else 64, or 32
+// where 64 would leave most SMs with a tile or two (three 13-node trees of 8/2 heads of 64 over
+// 333 shared + 0..300 keys: 32 rows 15.9 us, 64 rows 18.5; eight 64-node trees of 32/8 heads
+// over 1000 shared + 0..500: 580 and 429).  Key tiles are
 // divided so that there are about five CTAs for each SM.
 struct PagedF32Plan {
   int rt, splits, tiles_own, tiles_sh;

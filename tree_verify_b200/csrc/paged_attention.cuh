@@ -24,9 +24,10 @@ struct PagedAttnParams {
 // 128 threads: thread (ty, tx) has rows ty + kTY i and, of a tile, keys tx + kTX j in S = Q K^T
 // and columns 4 tx + 4 kTX k in O += P V, so that operands come from shared memory 16 bytes at
 // a time without bank conflicts.  64-row tiles feed 8 to 13 multiply-adds with each float4 (23
-// TFLOP/s); 32 rows give small problems more CTAs, 16 and 4 rows are for single tokens, whose
-// cost is the cache's bytes and the latency of a tile (4 rows: one warp a row).  K and V tiles
-// are double-buffered by asynchronous copies, which fill rows that are not there with zeros.
+// to 25 TFLOP/s of the pipe's 74); 32 rows give small problems more CTAs (with heads of 128
+// they spill 16 bytes a thread), 16 and 4 rows are for single tokens, whose cost is the cache's
+// bytes and the latency of a tile (4 rows: one warp a row).  K and V tiles are double-buffered
+// by asynchronous copies, which fill rows that are not there with zeros.
 
 struct PagedF32Params {
   PagedAttnParams a;

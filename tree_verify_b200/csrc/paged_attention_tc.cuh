@@ -34,8 +34,9 @@
 // Measured, main kernel and merge: 64 nodes x 8 sequences, 32/8 heads of 128, 8192 shared and
 // 131..512 own keys: 82 us, 870 TFLOP/s; there the softmax chain of a tile (some 890
 // instructions a thread) bounds it, beside 2,048 of 3,750 clocks of MMAs.  60 nodes x 16
-// sequences of 32/32 heads over 500 + 12..3596 keys: 123 us, 4.2 TB/s, a tile's chain of loads,
-// MMAs and softmax.  One token over 4097 keys: 14.3 us, latency.
+// sequences of 32/32 heads over 500 + 12..3596 keys: 123.5 us, 4.15 TB/s, a tile's chain of
+// loads, MMAs and softmax.  One token of each of 32 sequences of 32/8 heads over 2000..6000
+// keys: 93 us, 5.6 TB/s, HBM.  One token over 4097 keys: 14.6 us, latency.
 #pragma once
 
 #include "attention.cuh"
@@ -89,6 +90,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedTcParams& p, int b) {
 
 // Units of a key tile for `nrow` row tiles: a pair costs about 3,750 clocks, bound by its
 // softmax and MMAs; a single row tile half of that, or 2,800 while its K/V come from HBM.
+// (All measured with heads of 128; heads of 64 are cut by the same weights, unmeasured.)
 __device__ __forceinline__ int paged_tile_units(int nrow) { return nrow == 2 ? 4 : 3; }
 // Units of `T` tiles over `rb` row tiles of one kv head.
 __device__ __forceinline__ int64_t paged_head_units(int T, int rb) {
